@@ -561,6 +561,8 @@ int run_bwd(const void* q, const void* k, const void* v, const void* o, const fl
 
 }  // namespace
 
+#include "fa_layer_api.cuh"
+
 extern "C" {
 
 int fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -595,6 +597,7 @@ const char* fa_strerror(int status) {
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "kernel gave up on a bounded wait";
     case FA_ERR_SEQLENS: return "cu_seqlens out of range (seen by the kernel)";
+    case FA_ERR_POSITIONS: return "position outside the cos / sin table (seen by the kernel)";
     case FA_ERR_DEVICE: return "current device is not sm_100";
     default: return "unknown status";
   }
@@ -619,7 +622,8 @@ int fa_device_status(int clear, unsigned int* detail) {
   }
   if (detail) *detail = word;
   if (word == 0) return FA_OK;
-  return (word >> 8) == kRoleArgs ? FA_ERR_SEQLENS : FA_ERR_TIMEOUT;
+  if ((word >> 8) != kRoleArgs) return FA_ERR_TIMEOUT;
+  return (word & 0xffu) == kSitePositions ? FA_ERR_POSITIONS : FA_ERR_SEQLENS;
 }
 
 int fa_debug_watchdog_selftest(unsigned long long limit_ns, struct CUstream_st* stream) {

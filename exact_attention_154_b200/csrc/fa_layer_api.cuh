@@ -1,0 +1,225 @@
+// fa_layer_api.cuh -- host side of the entry points around the attention
+// itself (norm and rotation of queries and keys); part of fa_api.cu, whose
+// device state and checks it uses.
+#pragma once
+
+#include "fa_rope.cuh"
+
+namespace {
+
+constexpr long long kMaxElems = 1ll << 46;  // largest element offset of an operand
+
+// Strides {batch, head, row} in elements of a [B, H, N, d] operand; nullptr:
+// contiguous.  They must keep every row 16-byte aligned; the stride of a
+// dimension of size 1 is not used.
+struct Strides {
+  long long b, h, n;
+};
+int read_strides(const long long* s, int B, int H, int N, int d, Strides* out) {
+  *out = {(long long)H * N * d, (long long)N * d, d};
+  if ((double)B * H * N * d > (double)kMaxElems) return FA_ERR_ARG;
+  if (s == nullptr) return FA_OK;
+  const int sizes[3] = {B, H, N};
+  long long* to[3] = {&out->b, &out->h, &out->n};
+  for (int i = 0; i < 3; ++i) {
+    if (sizes[i] == 1) {
+      *to[i] = d;  // any valid value
+      continue;
+    }
+    if (s[i] < d) return FA_ERR_ARG;
+    if (s[i] % 8 != 0) return FA_ERR_ALIGN;
+    *to[i] = s[i];
+  }
+  // every element's offset must fit the index type used on the device
+  long long last = d;
+  for (int i = 0; i < 3; ++i) {
+    if (sizes[i] > 1 && *to[i] > kMaxElems / (sizes[i] - 1)) return FA_ERR_ARG;
+    last += (sizes[i] - 1) * *to[i];
+  }
+  return last > kMaxElems ? FA_ERR_ARG : FA_OK;
+}
+
+struct RopeArgs {
+  const void *x[2], *g[2], *w[2];
+  void *y[2], *dw[2];
+  const long long *xs[2], *gs[2], *ys[2];
+  const float *cos, *sin;
+  const int* positions;
+  float* parts;
+  int max_pos, weight_dtype, B, H, Hk, N, d, rot, interleaved, dtype;
+  float eps;
+};
+
+template <int HD, bool BF16, bool INTER, bool BWD>
+int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
+  constexpr int kTokens = 32 / (HD / 8), kWarps = kRopeThreads / 32;
+  const int HT = p.op[0].heads + p.op[1].heads;
+  const long long groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
+  // heads a warp walks over: more of them share the loaded cos / sin, fewer
+  // give a small call more warps
+  int hpw = 1;
+  while (hpw < 8 && hpw < HT && groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
+    hpw *= 2;
+  p.heads_per_warp = hpw;
+  p.chunks = (HT + hpw - 1) / hpw;
+  p.items = groups * p.chunks;
+  const long long ctas = (p.items + kWarps - 1) / kWarps;
+  const long long most = BWD ? FA_NORM_ROPE_PARTS : 1 << 20;
+  const int grid = (int)(ctas < most ? ctas : most);
+  qk_norm_rope_kernel<HD, BF16, INTER, BWD><<<grid, kRopeThreads, 0, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (BWD && (p.op[0].w != nullptr || p.op[1].w != nullptr)) {
+    norm_weight_sum_kernel<BF16><<<2 * d / 32, 256, 0, stream>>>(p.parts, grid, d, p.op[0].dw,
+                                                                p.op[1].dw, p.w_fp32);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+template <int HD, bool BWD>
+int launch_rope_types(RopeParams& p, DeviceState& st, const RopeArgs& a, cudaStream_t stream) {
+  if (a.dtype == FA_BF16)
+    return a.interleaved ? launch_rope<HD, true, true, BWD>(p, st, a.d, stream)
+                         : launch_rope<HD, true, false, BWD>(p, st, a.d, stream);
+  return a.interleaved ? launch_rope<HD, false, true, BWD>(p, st, a.d, stream)
+                       : launch_rope<HD, false, false, BWD>(p, st, a.d, stream);
+}
+
+template <bool BWD>
+int run_rope(const RopeArgs& a, cudaStream_t stream) {
+  if (a.dtype != FA_FP16 && a.dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (a.d != 64 && a.d != 128 && a.d != 256) return FA_ERR_HEADDIM;
+  if (a.B < 1 || a.H < 1 || a.Hk < 1 || a.N < 1 || a.max_pos < 1) return FA_ERR_ARG;
+  if (a.H > 65535 || a.Hk > 65535 || (long long)a.B * a.N > 0x7fffffffLL) return FA_ERR_ARG;
+  if (a.rot < 16 || a.rot > a.d || a.rot % 16 != 0) return FA_ERR_ARG;
+  if (a.interleaved != 0 && a.interleaved != 1) return FA_ERR_ARG;
+  if (!std::isfinite(a.eps) || a.eps < 0.f) return FA_ERR_ARG;
+  if (!a.cos || !a.sin) return FA_ERR_ARG;
+  if (a.positions == nullptr && a.N > a.max_pos) return FA_ERR_ARG;
+  const bool normed = a.w[0] != nullptr || a.w[1] != nullptr;
+  if (normed && a.weight_dtype != a.dtype && a.weight_dtype != FA_FP32) return FA_ERR_DTYPE;
+  if (!aligned16(a.cos) || !aligned16(a.sin) || !aligned4(a.positions)) return FA_ERR_ALIGN;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int i = 0; i < 2; ++i) {
+    // without a norm the gradient does not need the input itself
+    const bool needs_x = !BWD || a.w[i] != nullptr;
+    if ((needs_x && !a.x[i]) || !a.y[i]) return FA_ERR_ARG;
+    if (BWD && (!a.g[i] || (a.w[i] && !a.dw[i]))) return FA_ERR_ARG;
+    for (const void* t : {a.x[i], a.g[i], static_cast<const void*>(a.y[i]), a.w[i]})
+      if (!aligned16(t)) return FA_ERR_ALIGN;
+    if (!aligned4(a.dw[i])) return FA_ERR_ALIGN;
+    RopeOperand& o = p.op[i];
+    o.heads = i == 0 ? a.H : a.Hk;
+    Strides s;
+    int rc = read_strides(a.xs[i], a.B, o.heads, a.N, a.d, &s);
+    if (rc != FA_OK) return rc;
+    o.xb = s.b, o.xh = s.h, o.xn = s.n;
+    if ((rc = read_strides(a.ys[i], a.B, o.heads, a.N, a.d, &s)) != FA_OK) return rc;
+    o.yb = s.b, o.yh = s.h, o.yn = s.n;
+    if ((rc = read_strides(a.gs[i], a.B, o.heads, a.N, a.d, &s)) != FA_OK) return rc;
+    o.gb = s.b, o.gh = s.h, o.gn = s.n;
+    o.x = a.x[i], o.g = a.g[i], o.y = a.y[i], o.w = a.w[i], o.dw = a.w[i] ? a.dw[i] : nullptr;
+  }
+  if (BWD && (!a.parts || !aligned4(a.parts))) return a.parts ? FA_ERR_ALIGN : FA_ERR_ARG;
+  p.cos = a.cos, p.sin = a.sin, p.positions = a.positions, p.parts = a.parts;
+  p.B = a.B, p.N = a.N, p.max_pos = a.max_pos, p.rot = a.rot, p.eps = a.eps;
+  p.w_fp32 = a.weight_dtype == FA_FP32;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  const int rc = device_state(&st, &dev);
+  if (rc != FA_OK) return rc;
+  switch (a.d) {
+    case 64: return launch_rope_types<64, BWD>(p, *st, a, stream);
+    case 128: return launch_rope_types<128, BWD>(p, *st, a, stream);
+    default: return launch_rope_types<256, BWD>(p, *st, a, stream);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                    const long long* q_strides, const long long* k_strides,
+                    const long long* qo_strides, const long long* ko_strides, const float* cos,
+                    const float* sin, const int* positions, int max_pos, const void* q_weight,
+                    const void* k_weight, int weight_dtype, float eps, int B, int H, int Hk, int N,
+                    int d, int rot, int interleaved, int dtype, struct CUstream_st* stream) {
+  RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x[0] = q, a.x[1] = k, a.y[0] = q_out, a.y[1] = k_out;
+  a.xs[0] = q_strides, a.xs[1] = k_strides, a.ys[0] = qo_strides, a.ys[1] = ko_strides;
+  a.cos = cos, a.sin = sin, a.positions = positions, a.max_pos = max_pos;
+  a.w[0] = q_weight, a.w[1] = k_weight, a.weight_dtype = weight_dtype, a.eps = eps;
+  a.B = B, a.H = H, a.Hk = Hk, a.N = N, a.d = d, a.rot = rot;
+  a.interleaved = interleaved, a.dtype = dtype;
+  return run_rope<false>(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                        void* dq, void* dk, void* dq_weight, void* dk_weight,
+                        const long long* dqo_strides, const long long* dko_strides,
+                        const long long* q_strides, const long long* k_strides, const float* cos,
+                        const float* sin, const int* positions, int max_pos, const void* q_weight,
+                        const void* k_weight, int weight_dtype, float eps, float* workspace, int B,
+                        int H, int Hk, int N, int d, int rot, int interleaved, int dtype,
+                        struct CUstream_st* stream) {
+  RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.g[0] = dq_out, a.g[1] = dk_out, a.x[0] = q, a.x[1] = k, a.y[0] = dq, a.y[1] = dk;
+  a.dw[0] = dq_weight, a.dw[1] = dk_weight, a.parts = workspace;
+  a.gs[0] = dqo_strides, a.gs[1] = dko_strides, a.xs[0] = q_strides, a.xs[1] = k_strides;
+  a.cos = cos, a.sin = sin, a.positions = positions, a.max_pos = max_pos;
+  a.w[0] = q_weight, a.w[1] = k_weight, a.weight_dtype = weight_dtype, a.eps = eps;
+  a.B = B, a.H = H, a.Hk = Hk, a.N = N, a.d = d, a.rot = rot;
+  a.interleaved = interleaved, a.dtype = dtype;
+  return run_rope<true>(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_rope_table(float* cos, float* sin, int max_pos, int rot, double base, int scaling,
+                  double factor, int original_max_pos, struct CUstream_st* stream) {
+  if (!cos || !sin || max_pos < 1) return FA_ERR_ARG;
+  if (rot < 16 || rot > 256 || rot % 16 != 0) return FA_ERR_ARG;
+  if (!std::isfinite(base) || !(base > 1.0)) return FA_ERR_ARG;
+  if (scaling < FA_ROPE_PLAIN || scaling > FA_ROPE_YARN) return FA_ERR_ARG;
+  if (scaling != FA_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0)) return FA_ERR_ARG;
+  if (scaling == FA_ROPE_YARN && original_max_pos < 1) return FA_ERR_ARG;
+  if (!aligned16(cos) || !aligned16(sin)) return FA_ERR_ALIGN;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  const int rc = device_state(&st, &dev);
+  if (rc != FA_OK) return rc;
+  RopeTableParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.cos = cos, p.sin = sin, p.max_pos = max_pos, p.half = rot / 2, p.factor = 1.0;
+  if (scaling == FA_ROPE_NTK) base *= std::pow(factor, rot / (rot - 2.0));
+  // yarn: the pair whose wavelength fits original_max_pos `turns` times
+  const double two_pi = 6.283185307179586;
+  double low = 0.0, high = 1.0;
+  if (scaling == FA_ROPE_YARN) {
+    auto pair_of = [&](double turns) {
+      return rot * std::log(original_max_pos / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    low = std::fmax(std::floor(pair_of(32.0)), 0.0);
+    high = std::fmin(std::ceil(pair_of(1.0)), rot - 1.0);
+    if (high <= low) high = low + 0.001;
+    p.factor = 0.1 * std::log(factor) + 1.0;
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == FA_ROPE_LINEAR) f /= factor;
+    if (scaling == FA_ROPE_YARN) {
+      // fast pairs keep their frequency, slow ones are interpolated
+      const double slow = std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0);
+      f = f / factor * slow + f * (1.0 - slow);
+    }
+    p.inv_freq[i] = f;
+  }
+  const long long blocks = ((long long)max_pos * p.half + 255) / 256;
+  const int grid = (int)(blocks < 16ll * st->sm_count ? blocks : 16ll * st->sm_count);
+  rope_table_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

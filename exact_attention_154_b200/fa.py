@@ -23,7 +23,11 @@ _lib = None
 FA_OK = 0
 FA_ERR_ARG, FA_ERR_ALIGN, FA_ERR_HEADDIM, FA_ERR_DTYPE = -1, -2, -3, -4
 FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE = -5, -6, -7, -8
-FA_ERR_SEQLENS = -9
+FA_ERR_SEQLENS, FA_ERR_POSITIONS = -9, -10
+
+FA_FP32 = 3
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+NORM_ROPE_PARTS = 592
 
 #: every function the C header declares, with (restype, argtypes)
 _VP, _FP, _I, _F = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
@@ -40,6 +44,9 @@ SIGNATURES = {
                     _VP]),
     "fa_bwd_noalloc": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I,
                             _I, _VP]),
+    "fa_qk_norm_rope": (_I, [_VP] * 11 + [_I, _VP, _VP, _I, _F] + [_I] * 8 + [_VP]),
+    "fa_qk_norm_rope_bwd": (_I, [_VP] * 15 + [_I, _VP, _VP, _I, _F, _FP] + [_I] * 8 + [_VP]),
+    "fa_rope_table": (_I, [_FP, _FP, _I, _I, ctypes.c_double, _I, ctypes.c_double, _I, _VP]),
     "fa_strerror": (ctypes.c_char_p, [_I]),
     "fa_device_status": (_I, [_I, ctypes.POINTER(ctypes.c_uint)]),
     "fa_debug_watchdog_selftest": (_I, [ctypes.c_ulonglong, _VP]),
@@ -336,6 +343,173 @@ def bwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tens
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_noalloc")
     return dq, dk, dv
+
+
+def _check_rows(t: torch.Tensor, name: str, dtype=None):
+    """A 16-bit CUDA tensor [B, H, N, d] whose rows are adjacent elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be float16 or bfloat16, one type for all operands")
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be [B, H, N, d] with adjacent elements in a row")
+
+
+def _strides(t: torch.Tensor):
+    """The (batch, head, row) strides argument of the C ABI; None when contiguous."""
+    return None if t.is_contiguous() else (ctypes.c_longlong * 3)(*t.stride()[:3])
+
+
+def _fresh_rows(t: torch.Tensor):
+    """Whether the rows of [B, H, N, d] tensor ``t`` surely do not overlap: its
+    dimensions, ordered by stride, each step over the one before."""
+    need = 0
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
+                               key=lambda x: x[1]):
+        if stride <= need:
+            return False
+        need += (size - 1) * stride
+    return True
+
+
+def _table(cos, sin, positions, B, N):
+    """Checks of the cos / sin table and the positions; (max_pos, rot)."""
+    for name, t in (("cos", cos), ("sin", sin)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [max_pos, rot / 2] tensor")
+    if cos.shape != sin.shape:
+        raise ValueError("cos and sin must share one shape")
+    if positions is not None and (not isinstance(positions, torch.Tensor)
+                                  or positions.dtype != torch.int32
+                                  or positions.shape != (B, N) or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 [B, N] tensor")
+    return cos.shape[0], 2 * cos.shape[1]
+
+
+def _weights(q_weight, k_weight, d, dtype):
+    """Checks of the norm weights; the type code the library is told."""
+    given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    for name, w in given:
+        if not isinstance(w, torch.Tensor) or w.shape != (d,) or not w.is_contiguous() \
+                or w.dtype not in (dtype, torch.float32) or w.dtype != given[0][1].dtype:
+            raise ValueError(f"{name} must be a contiguous [d] tensor of the operands' type or "
+                             "float32, both weights of one type")
+    return FA_FP32 if given and given[0][1].dtype == torch.float32 else _DT[dtype]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",
+               factor: float = 1.0, original_max_pos: int = 0, device="cuda"):
+    """``(cos, sin)``, each ``[max_pos, rot / 2]`` fp32: the table of
+    :func:`qk_norm_rope` for angles ``p * base ** (-2 i / rot)``.
+
+    ``scaling`` for contexts longer than trained on: ``"linear"`` (frequencies
+    over ``factor``), ``"ntk"`` (a larger base), ``"yarn"`` (slow pairs
+    interpolated, fast ones kept; needs ``original_max_pos``)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("device must be a CUDA device")
+    if max_pos < 1 or rot < 2:
+        raise ValueError("max_pos and rot must be positive")
+    cos = torch.empty((max_pos, rot // 2), device=dev, dtype=torch.float32)
+    sin = torch.empty_like(cos)
+    with _on(cos.device):
+        rc = load().fa_rope_table(cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base),
+                                  ROPE_SCALING[scaling], float(factor), int(original_max_pos),
+                                  _stream_ptr(cos))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rope_table")
+    return cos, sin
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                 positions: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None):
+    """RMS norm of every head's query and key and the rotation by position.
+
+    ``q`` is ``[B, H, N, d]``, ``k`` ``[B, Hk, N, d]``, of any strides with
+    adjacent row elements (views of a packed projection, ``transpose(1, 2)`` of
+    ``[B, N, H, d]``).  ``cos``, ``sin``: ``[max_pos, rot / 2]`` fp32
+    (:func:`rope_table`); ``positions`` int32 ``[B, N]`` (None: the row index).
+    ``q_weight``, ``k_weight``: ``[d]``, or None to leave that operand
+    unnormalised.  Returns ``(q_out, k_out)``, contiguous unless given; they
+    may be ``q`` and ``k`` themselves."""
+    _check_rows(q, "q")
+    _check_rows(k, "k", q.dtype)
+    B, H, N, d = q.shape
+    Hk = k.shape[1]
+    if k.shape != (B, Hk, N, d):
+        raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
+    max_pos, rot = _table(cos, sin, positions, B, N)
+    wt = _weights(q_weight, k_weight, d, q.dtype)
+    if q_out is None:
+        q_out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+    if k_out is None:
+        k_out = torch.empty((B, Hk, N, d), device=q.device, dtype=q.dtype)
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        _check_rows(t, name, q.dtype)
+        if t.shape != like.shape or not _fresh_rows(t):
+            raise ValueError(f"{name} must have its input's shape and rows that do not overlap")
+    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("cos", cos), ("sin", sin),
+                                           ("positions", positions), ("q_weight", q_weight),
+                                           ("k_weight", k_weight), ("q_out", q_out),
+                                           ("k_out", k_out)) if t is not None])
+    with _on(dev):
+        rc = load().fa_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _strides(q),
+            _strides(k), _strides(q_out), _strides(k_out), cos.data_ptr(), sin.data_ptr(),
+            _ptr(positions), max_pos, _ptr(q_weight), _ptr(k_weight), wt, float(eps), B, H, Hk, N,
+            d, rot, int(bool(interleaved)), _DT[q.dtype], _stream_ptr(q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor | None = None,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                     eps: float = 1e-6, interleaved: bool = False):
+    """Gradient of :func:`qk_norm_rope` for gradients ``dq_out``, ``dk_out`` of
+    its results; ``q``, ``k`` and the rest are the forward's arguments.
+    Returns ``(dq, dk, dq_weight, dk_weight)``, the first two contiguous, the
+    last two None where the weight is None."""
+    _check_rows(q, "q")
+    B, H, N, d = q.shape
+    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+    for name, t, shape in (("k", k, (B, Hk, N, d)), ("dq_out", dq_out, q.shape),
+                           ("dk_out", dk_out, (B, Hk, N, d))):
+        _check_rows(t, name, q.dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name} does not match q and k")
+    max_pos, rot = _table(cos, sin, positions, B, N)
+    wt = _weights(q_weight, k_weight, d, q.dtype)
+    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("dq_out", dq_out),
+                                           ("dk_out", dk_out), ("cos", cos), ("sin", sin),
+                                           ("positions", positions), ("q_weight", q_weight),
+                                           ("k_weight", k_weight)) if t is not None])
+    dq = torch.empty((B, H, N, d), device=dev, dtype=q.dtype)
+    dk = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    ws = torch.empty((NORM_ROPE_PARTS, 2, d), device=dev, dtype=torch.float32)
+    with _on(dev):
+        rc = load().fa_qk_norm_rope_bwd(
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), _ptr(dqw), _ptr(dkw), _strides(dq_out), _strides(dk_out), _strides(q),
+            _strides(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions), max_pos, _ptr(q_weight),
+            _ptr(k_weight), wt, float(eps), ws.data_ptr(), B, H, Hk, N, d, rot,
+            int(bool(interleaved)), _DT[q.dtype], _stream_ptr(q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
 
 
 def device_status(clear: bool = True):

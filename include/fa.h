@@ -54,11 +54,21 @@ enum fa_status {
   FA_ERR_CUDA = -6,        /* a CUDA runtime / driver call failed */
   FA_ERR_TIMEOUT = -7,     /* a kernel gave up on a bounded wait */
   FA_ERR_DEVICE = -8,      /* the current device is not sm_100 (B200 class) */
-  FA_ERR_SEQLENS = -9      /* (fa_device_status) a kernel met cu_seqlens out of range */
+  FA_ERR_SEQLENS = -9,     /* (fa_device_status) a kernel met cu_seqlens or cache lengths out of range */
+  FA_ERR_POSITIONS = -10   /* (fa_device_status) a kernel met a position outside the cos / sin table */
 };
 
-/* FA_E4M3 (fp8 e4m3 operands) is accepted by fa_fwd_fp8 only. */
-enum fa_dtype { FA_FP16 = 0, FA_BF16 = 1, FA_E4M3 = 2 };
+/*
+ * FA_E4M3 (fp8 e4m3 operands) is accepted by fa_fwd_fp8 only, FA_FP32 as the
+ * type of fa_qk_norm_rope's weights only.
+ */
+enum fa_dtype { FA_FP16 = 0, FA_BF16 = 1, FA_E4M3 = 2, FA_FP32 = 3 };
+
+/* How fa_rope_table scales the rotation for contexts longer than trained on. */
+enum fa_rope_scaling { FA_ROPE_PLAIN = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_YARN = 3 };
+
+/* fa_qk_norm_rope_bwd: rows of [2, d] fp32 its workspace holds. */
+enum { FA_NORM_ROPE_PARTS = 592 };
 
 /*
  * Attention forward on separate Q, K, V.
@@ -232,6 +242,89 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
                    const void *dout, void *dq, void *dk, void *dv, int B, int H, int N, int d,
                    float scale, int causal, int dtype, struct CUstream_st *stream);
 
+/*
+ * RMS norm of every head's query and key and the rotation by position, in one
+ * pass: what turns a projection's output into the q and k that fa_fwd takes.
+ * For a row x of q (of k) at position p, weight w = q_weight (k_weight):
+ *
+ *     y = x * w / sqrt(mean(x^2) + eps)              (w == NULL: y = x)
+ *     out[a_i] = y[a_i] cos[p, i] - y[b_i] sin[p, i]
+ *     out[b_i] = y[a_i] sin[p, i] + y[b_i] cos[p, i]     i < rot / 2
+ *     out[c] = y[c]                                      c >= rot
+ *
+ * with (a_i, b_i) = (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved.
+ * Statistics and products are fp32; the result is rounded once.
+ *
+ *   q, k         : [B, H, N, d] and [B, Hk, N, d], element type `dtype`
+ *   q_out, k_out : the same shapes (written); may be the inputs themselves
+ *   *_strides    : host pointers to {batch, head, row} strides in elements, or
+ *                  NULL for a contiguous tensor; the d elements of a row are
+ *                  always adjacent.  Strides are >= d and multiples of 8; that of a
+ *                  dimension of size 1 is ignored.  Rows of an output must not
+ *                  overlap one another, nor an input's other rows.
+ *   cos, sin     : [max_pos, rot / 2] fp32, contiguous (see fa_rope_table)
+ *   positions    : [B, N] int32, or NULL: row n is at position n (then
+ *                  N <= max_pos).  Read on the device: the rows of a token
+ *                  whose position lies outside [0, max_pos) are not written,
+ *                  and fa_device_status() then returns FA_ERR_POSITIONS.
+ *   q_weight, k_weight : [d] of type `weight_dtype` (`dtype` or FA_FP32), or
+ *                  NULL: that operand is not normalised
+ *   d            : 64, 128 or 256;  rot: a multiple of 16, 16 .. d
+ *   eps          : finite, >= 0
+ *   H, Hk        : independent (1 .. 65535)
+ *
+ * q, k, outputs, tables and weights are 16-byte aligned, positions 4-byte.
+ */
+int fa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                    const long long *q_strides, const long long *k_strides,
+                    const long long *qo_strides, const long long *ko_strides, const float *cos,
+                    const float *sin, const int *positions, int max_pos, const void *q_weight,
+                    const void *k_weight, int weight_dtype, float eps, int B, int H, int Hk, int N,
+                    int d, int rot, int interleaved, int dtype, struct CUstream_st *stream);
+
+/*
+ * Gradient of fa_qk_norm_rope for gradients dq_out, dk_out of its results:
+ *
+ *   q, k       : the forward's inputs (not read, and may be NULL, where the
+ *                weight is NULL)
+ *   dq, dk     : [B, H, N, d] and [B, Hk, N, d] contiguous (written); may be
+ *                dq_out and dk_out themselves when those are contiguous
+ *   dq_weight, dk_weight : [d] of type `weight_dtype` (written), required where
+ *                the weight is given
+ *   workspace  : FA_NORM_ROPE_PARTS * 2 * d fp32, caller-owned scratch
+ *   other arguments as fa_qk_norm_rope.
+ *
+ * The weights' gradients are summed in fp32 in an order that does not change
+ * from call to call.  A token whose position lies outside the table adds
+ * nothing to them, and its rows of dq and dk are not written.
+ */
+int fa_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                        void *dq, void *dk, void *dq_weight, void *dk_weight,
+                        const long long *dqo_strides, const long long *dko_strides,
+                        const long long *q_strides, const long long *k_strides, const float *cos,
+                        const float *sin, const int *positions, int max_pos, const void *q_weight,
+                        const void *k_weight, int weight_dtype, float eps, float *workspace, int B,
+                        int H, int Hk, int N, int d, int rot, int interleaved, int dtype,
+                        struct CUstream_st *stream);
+
+/*
+ * The cos / sin table of fa_qk_norm_rope: cos[p, i] = cos(p f_i) and sin[p, i],
+ * f_i = base^(-2 i / rot), computed in fp64 and rounded once.
+ *
+ *   cos, sin : [max_pos, rot / 2] fp32 (written), 16-byte aligned
+ *   rot      : a multiple of 16, 16 .. 256;  base > 1
+ *   scaling  : FA_ROPE_PLAIN   f_i as above (factor is not used)
+ *              FA_ROPE_LINEAR  f_i / factor (position interpolation)
+ *              FA_ROPE_NTK     base * factor^(rot / (rot - 2)) in place of base
+ *              FA_ROPE_YARN    f_i / factor for pairs that turn less than once in
+ *                  original_max_pos positions, f_i for those that turn more
+ *                  than 32 times, a linear blend over i between them, and cos
+ *                  and sin times 0.1 ln(factor) + 1 (the YaRN paper's recipe)
+ *   factor   : >= 1;  original_max_pos: >= 1 (YARN only)
+ */
+int fa_rope_table(float *cos, float *sin, int max_pos, int rot, double base, int scaling,
+                  double factor, int original_max_pos, struct CUstream_st *stream);
+
 /* Static text for a status code. */
 const char *fa_strerror(int status);
 
@@ -239,7 +332,8 @@ const char *fa_strerror(int status);
  * Reads (and, if clear != 0, resets) the current device's watchdog word.
  * Synchronises the current device first.  Returns FA_OK, FA_ERR_TIMEOUT when a
  * kernel gave up on a bounded wait, FA_ERR_SEQLENS when fa_fwd_varlen met
- * offsets out of range (`*detail`, if not NULL, receives the (role << 8) | site
+ * offsets out of range, FA_ERR_POSITIONS when fa_qk_norm_rope met a position
+ * outside its table (`*detail`, if not NULL, receives the (role << 8) | site
  * code), or FA_ERR_CUDA.
  */
 int fa_device_status(int clear, unsigned int *detail);
