@@ -118,6 +118,9 @@ struct FwdParams {
   int num_qblocks;   // query blocks per (b, h) (of the longest sequence)
   int num_tiles;     // B * H * num_qblocks
   unsigned long long wait_limit_ns;
+  // Kernels with SINKS only: key j < sinks is visible from every query i >= j
+  // whatever the window; query head h reads key / value head h / group.
+  int sinks, group;
 };
 
 // Bounded wait on an mbarrier phase.  Gives up when the CTA-wide abort flag
@@ -223,6 +226,12 @@ struct FwdCfg {
 // needs the key blocks [lo[s], hi[s]) (empty: lo == hi == 0); the work tile
 // streams their union [lo_u, lo_u + n_u), which is contiguous because the Q
 // tiles are adjacent and every row sees its own key.
+//
+// With SINKS a tile also needs the blocks [0, ns) that hold the sinks (those
+// below hi[s]), and the work tile streams n_u blocks: [0, ns), then from
+// gap_end = max(ns, lo[0]) on.  Tile 0 uses every streamed block up to its
+// last (lo[0] <= lo[1] <= hi[0]), so a block's users are tile 0, tile 1 or
+// both, and after tile 0's last only tile 1.
 struct TileInfo {
   int b, h, q0;  // q0: first query row, relative to the sequence
   int len;       // the sequence's length (queries = keys)
@@ -230,10 +239,29 @@ struct TileInfo {
   int bc;        // tensor-map batch coordinate
   int lo[2], hi[2];
   int lo_u, n_u;
+  int hk;           // key / value head (SINKS; else h)
+  int ns, gap_end;  // SINKS
 };
 
+template <bool SINKS>
 __device__ __forceinline__ bool in_range(const TileInfo& ti, int s, int j) {
+  if constexpr (SINKS) return j < ti.hi[s] && (j < ti.ns || j >= ti.lo[s]);
   return j >= ti.lo[s] && j < ti.hi[s];
+}
+// The jj-th key block the work tile streams.
+template <bool SINKS>
+__device__ __forceinline__ int block_of(const TileInfo& ti, int jj) {
+  if constexpr (SINKS) return jj < ti.ns ? jj : jj - ti.ns + ti.gap_end;
+  return ti.lo_u + jj;
+}
+// The first key block of Q tile s, and the one after its block j.
+template <bool SINKS>
+__device__ __forceinline__ int first_block(const TileInfo& ti, int s) {
+  return SINKS && ti.ns > 0 ? 0 : ti.lo[s];
+}
+template <bool SINKS>
+__device__ __forceinline__ int block_after(const TileInfo& ti, int s, int j) {
+  return SINKS && j + 1 == ti.ns ? max(ti.ns, ti.lo[s]) : j + 1;
 }
 
 // Key blocks [lo, hi) a 128-row Q tile starting at row r0 of a sequence of
@@ -251,7 +279,7 @@ __device__ __forceinline__ void key_range(const FwdParams& p, int len, int r0, i
   hi = p.window_right < 0 ? nkv : min(len - 1, last_row + p.window_right) / BN + 1;
 }
 
-template <int QS>
+template <int QS, bool SINKS>
 __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
   TileInfo ti;
   int bh, qblock;
@@ -293,6 +321,15 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     ti.lo[1] = ti.hi[1] = 0;
   ti.lo_u = ti.lo[0];
   ti.n_u = ti.hi[0] == 0 ? 0 : max(ti.hi[0], ti.hi[1]) - ti.lo[0];
+  if constexpr (SINKS) {
+    ti.hk = ti.h / p.group;
+    ti.ns = p.window_left < 0 ? 0 : (p.sinks + BN - 1) / BN;
+    ti.gap_end = max(ti.ns, ti.lo[0]);
+    if (ti.hi[0] != 0) ti.n_u = max(ti.hi[0], ti.hi[1]) - (ti.gap_end - ti.ns);
+  } else {
+    ti.hk = ti.h;
+    ti.ns = ti.gap_end = 0;
+  }
   return ti;
 }
 
@@ -308,10 +345,12 @@ __host__ __device__ __forceinline__ int ring_v(int j, int n) { return j < n - 1 
 // j + 1, ...  Tile 0's range starts first, so it is every work tile's first
 // user.  Returns the tile of the use after (s, j), or -1 if (s, j) is the
 // work tile's last.
+template <bool SINKS>
 __device__ __forceinline__ int next_p_user(int s, int j, const TileInfo& ti) {
-  if (s == 0 && in_range(ti, 1, j)) return 1;
-  if (in_range(ti, 0, j + 1)) return 0;
-  if (in_range(ti, 1, j + 1)) return 1;
+  if (s == 0 && in_range<SINKS>(ti, 1, j)) return 1;
+  const int next = SINKS && j + 1 == ti.ns ? ti.gap_end : j + 1;
+  if (in_range<SINKS>(ti, 0, next)) return 0;
+  if (in_range<SINKS>(ti, 1, next)) return 1;
   return -1;
 }
 
@@ -363,7 +402,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------------ roles
-template <int HD, int QS, int KVS, int ELT>
+template <int HD, int QS, int KVS, int ELT, bool SINKS>
 __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
   const uint32_t bars = base + C::BAR_OFF;
@@ -391,7 +430,7 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
 #pragma unroll
     for (int c = 0; c < C::CHUNKS; ++c)
       tma_load_4d(base + C::SKV_OFF + slot * C::TILE_BYTES + c * C::CHUNK_BYTES, map, full,
-                  c * C::BOX, ti.row0 + row0, ti.h, ti.bc);
+                  c * C::BOX, ti.row0 + row0, ti.hk, ti.bc);
     ++kv_count;
     return true;
   };
@@ -411,11 +450,11 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS>(p, t);
+    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     if (ti.n_u == 0) continue;
     // The first K tile needs only a ring slot: request it before waiting for
     // the previous work tile to release the Q buffer, so the two loads overlap.
-    if (!(ok = load_kv(&p.tmap_k, ti.lo_u * BN, ti, true))) break;
+    if (!(ok = load_kv(&p.tmap_k, block_of<SINKS>(ti, 0) * BN, ti, true))) break;
     if (q_count > 0) {
       ok = wait_phase(bars + 8 * C::B_Q_EMPTY, (q_count - 1) & 1, abort_flag, p.wait_limit_ns,
                       (kRoleProducer << 8) | kSiteQEmpty);
@@ -430,9 +469,10 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
                     bars + 8 * C::B_Q_FULL, c * C::BOX, ti.row0 + ti.q0 + s * BM, ti.h, ti.bc);
     ++q_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      const int j = ti.lo_u + jj;
-      if (jj + 1 < ti.n_u && !(ok = load_kv(&p.tmap_k, (j + 1) * BN, ti, true))) break;
-      ok = load_kv(&p.tmap_v, j * BN, ti, false);
+      if (jj + 1 < ti.n_u &&
+          !(ok = load_kv(&p.tmap_k, block_of<SINKS>(ti, jj + 1) * BN, ti, true)))
+        break;
+      ok = load_kv(&p.tmap_v, block_of<SINKS>(ti, jj) * BN, ti, false);
     }
 #pragma unroll 1
     for (int s = 0; ok && s < QS; ++s)
@@ -463,7 +503,7 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
 
 // S thread, per work tile: S_s(0) for every Q tile s, then S_s(j+1) once the
 // softmax of tile s has read S_s(j) out of TMEM.
-template <int HD, int QS, int KVS, int ELT>
+template <int HD, int QS, int KVS, int ELT, bool SINKS>
 __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                            volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -516,7 +556,7 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS>(p, t);
+    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     if (ti.n_u == 0) continue;
     ok = wait_phase(bars + 8 * C::B_Q_FULL, q_count & 1, abort_flag, lim,
                     (kRoleMma << 8) | kSiteQFull);
@@ -525,12 +565,12 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
     if (!ok) break;
     const int kv0 = kv_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      const int j = ti.lo_u + jj;
+      const int j = block_of<SINKS>(ti, jj);
       const int k_idx = kv0 + ring_k(jj);
       if (!(ok = wait_kv(k_idx))) break;
 #pragma unroll 1
       for (int s = 0; s < QS; ++s)
-        if (ok && in_range(ti, s, j)) ok = issue_s(s, k_idx % KVS);
+        if (ok && in_range<SINKS>(ti, s, j)) ok = issue_s(s, k_idx % KVS);
       if (!ok) break;
       tc_commit(bars + 8 * (C::B_KV_EMPTY + k_idx % KVS));
       if (jj + 1 == ti.n_u) tc_commit(bars + 8 * C::B_Q_EMPTY);
@@ -549,7 +589,7 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
 // then tile 1, each once the softmax has written P_s(j) into the shared P
 // buffer; after each product the buffer is handed to the tile that uses it
 // next (which also tells that tile's softmax that O_s holds the product).
-template <int HD, int QS, int KVS, int ELT>
+template <int HD, int QS, int KVS, int ELT, bool SINKS>
 __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                             volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -600,11 +640,11 @@ __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS>(p, t);
+    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     if (ti.n_u == 0) continue;
     const int kv0 = kv_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      const int j = ti.lo_u + jj;
+      const int j = block_of<SINKS>(ti, jj);
       const int v_idx = kv0 + ring_v(jj, ti.n_u);
       ok = wait_phase(bars + 8 * (C::B_V_FULL + v_idx % KVS), (v_par >> (v_idx % KVS)) & 1u,
                       abort_flag, lim, (kRoleMma << 8) | kSiteKvFull);
@@ -612,10 +652,10 @@ __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       tc_fence_after_sync();
 #pragma unroll 1
       for (int s = 0; s < QS; ++s) {
-        if (!ok || !in_range(ti, s, j)) continue;
+        if (!ok || !in_range<SINKS>(ti, s, j)) continue;
         // the next work tile starts with tile 0
-        const int nxt = next_p_user(s, j, ti);
-        ok = issue_pv(s, v_idx % KVS, j > ti.lo[s], nxt < 0 ? 0 : nxt);
+        const int nxt = next_p_user<SINKS>(s, j, ti);
+        ok = issue_pv(s, v_idx % KVS, j > first_block<SINKS>(ti, s), nxt < 0 ? 0 : nxt);
         if (!ok) break;
         if (j == ti.hi[s] - 1) tc_commit(bars + 8 * (C::B_O_FINAL + s));
       }
@@ -733,7 +773,7 @@ __device__ __forceinline__ void store_p_half_e4m3(uint32_t p_base, int r, int hf
 
 // ALIBI: the scaled score of key j gets -slope[h] * |i - j| (in the log2
 // domain, -slope[h] * log2(e) * |i - j|) before the row max is taken.
-template <int HD, int QS, int KVS, int ELT, bool ALIBI>
+template <int HD, int QS, int KVS, int ELT, bool ALIBI, bool SINKS>
 __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                              volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -779,7 +819,7 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS>(p, t);
+    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     // ring slot of this tile's O and the parity of its reservation; every
     // group follows the reservations of both tiles
     int o_slot = -1;
@@ -809,7 +849,8 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
     if constexpr (ALIBI) nslope2 = -__ldg(p.alibi_slopes + ti.h) * 1.4426950408889634f;
     float m_ref = -INFINITY, l = 0.f;
 
-    for (int j = lo; j < hi; ++j) {
+    const int j0 = first_block<SINKS>(ti, s);
+    for (int j = j0; j < hi; j = block_after<SINKS>(ti, s, j)) {
       bool ok = wait_phase(bars + 8 * (C::B_S_FULL + s), s_par, abort_flag, lim,
                            (kRoleSoftmax << 8) | kSiteSFull);
       s_par ^= 1u;
@@ -825,13 +866,16 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       // tail, the causal diagonal, the edges of a local window.
       const bool need_mask =
           (j * BN + BN > ti.len) ||
-          (p.window_left >= 0 && j * BN < r_last - p.window_left) ||
+          (p.window_left >= 0 && j * BN < r_last - p.window_left &&
+           (!SINKS || j * BN + BN > p.sinks)) ||
           (p.window_right >= 0 && j * BN + BN - 1 > r_first + p.window_right);
       const int kbase = j * BN + 64 * hf;  // key of this thread's first column
       if (need_mask) {
         const int lo_c = vis_lo - kbase, hi_c = vis_hi - kbase;
+        const int sink_c = SINKS ? p.sinks - kbase : 0;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) sv[c] = (c >= lo_c && c < hi_c) ? sv[c] : -INFINITY;
+        for (int c = 0; c < 64; ++c)
+          sv[c] = ((c >= lo_c || (SINKS && c < sink_c)) && c < hi_c) ? sv[c] : -INFINITY;
       }
       float m_half;
       if constexpr (ALIBI) {
@@ -860,10 +904,10 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       // take the same decision from the same values.
       // A row with no visible key so far (m_ref = -inf: only possible at the
       // edges of a local window) has l = 0 and O = 0, so its alpha is 0.
-      const bool rescale = (j > lo) && (m_blk > m_ref + kLazyRescaleLog2);
-      const float m_new = (j == lo || rescale) ? m_blk : m_ref;
+      const bool rescale = (j > j0) && (m_blk > m_ref + kLazyRescaleLog2);
+      const float m_new = (j == j0 || rescale) ? m_blk : m_ref;
       const float alpha =
-          (j == lo || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);  // 1 when m_ref is kept
+          (j == j0 || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);  // 1 when m_ref is kept
       m_ref = m_new;
       const float neg_ref = (m_ref == -INFINITY) ? 0.f : -m_ref;
       const float sl2e = ALIBI ? 1.f : sl2;  // the ALiBi path holds scaled scores already
@@ -1012,7 +1056,7 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
 // waits until both softmax groups have staged their columns there, writes the
 // tile out with TMA stores, waits until the stores have read the slot and
 // releases it to the producer.
-template <int HD, int QS, int KVS, int ELT>
+template <int HD, int QS, int KVS, int ELT, bool SINKS>
 __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
   const uint32_t bars = base + C::BAR_OFF;
@@ -1023,7 +1067,7 @@ __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abor
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS>(p, t);
+    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     if (ti.n_u == 0) continue;
     const int kv0 = kv_count;
     kv_count += 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
@@ -1050,7 +1094,7 @@ __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abor
   bulk_wait_all();
 }
 
-template <int HD, int QS, int KVS, int ELT, bool ALIBI>
+template <int HD, int QS, int KVS, int ELT, bool ALIBI, bool SINKS = false>
 __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -1119,15 +1163,15 @@ __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
   }
 
   if (warp < C::SOFTMAX_WARPS) {
-    softmax_role<HD, QS, KVS, ELT, ALIBI>(p, base, tmem, abort_flag);
+    softmax_role<HD, QS, KVS, ELT, ALIBI, SINKS>(p, base, tmem, abort_flag);
   } else if (warp == C::PRODUCER_WARP) {
-    if (lane == 0) producer_role<HD, QS, KVS, ELT>(p, base, abort_flag);
+    if (lane == 0) producer_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
   } else if (warp == C::MMA_S_WARP) {
-    if (lane == 0) mma_s_role<HD, QS, KVS, ELT>(p, base, tmem, abort_flag);
+    if (lane == 0) mma_s_role<HD, QS, KVS, ELT, SINKS>(p, base, tmem, abort_flag);
   } else if (warp == C::MMA_PV_WARP) {
-    if (lane == 0) mma_pv_role<HD, QS, KVS, ELT>(p, base, tmem, abort_flag);
+    if (lane == 0) mma_pv_role<HD, QS, KVS, ELT, SINKS>(p, base, tmem, abort_flag);
   } else if (warp == C::STORE_WARP) {
-    if (lane == 0 && C::O_TMA) store_role<HD, QS, KVS, ELT>(p, base, abort_flag);
+    if (lane == 0 && C::O_TMA) store_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
   }
 
   tc_fence_before_sync();

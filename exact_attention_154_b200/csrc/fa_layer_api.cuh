@@ -1,6 +1,7 @@
 // fa_layer_api.cuh -- host side of the entry points around the attention
-// itself (norm and rotation of queries and keys); part of fa_api.cu, whose
-// device state and checks it uses.
+// itself (norm and rotation of queries and keys) and of the attention with a
+// causal window and sinks; part of fa_api.cu, whose device state and checks it
+// uses.
 #pragma once
 
 #include "fa_rope.cuh"
@@ -26,7 +27,7 @@ int read_strides(const long long* s, int B, int H, int N, int d, Strides* out) {
       *to[i] = d;  // any valid value
       continue;
     }
-    if (s[i] < d) return FA_ERR_ARG;
+    if (s[i] < d || s[i] >= 1ll << 39) return FA_ERR_ARG;  // a tensor map's limit is 2^40 bytes
     if (s[i] % 8 != 0) return FA_ERR_ALIGN;
     *to[i] = s[i];
   }
@@ -136,9 +137,226 @@ int run_rope(const RopeArgs& a, cudaStream_t stream) {
   }
 }
 
+// ------------------------------------------------ causal window and sinks
+
+struct SinksState {
+  std::atomic<bool> fwd_attr[6] = {};
+  std::atomic<bool> bwd_attr[8] = {};
+};
+SinksState g_sinks[kMaxDevices];
+
+// Checks of a window-and-sinks problem; brings window and sinks into the range
+// the kernels use (-1: every earlier key is visible).
+int check_sinks(int B, int H, int Hk, int N, int d, float* scale, int* window, int* sinks,
+                int dtype) {
+  if (dtype == FA_E4M3) return FA_ERR_DTYPE;
+  const int rc = check_common(B, H, N, d, scale, 1, dtype);
+  if (rc != FA_OK) return rc;
+  if (Hk < 1 || H % Hk != 0 || N > 1 << 30) return FA_ERR_ARG;
+  if (*window < -1 || *sinks < 0) return FA_ERR_ARG;
+  if (*window >= N - 1) *window = -1;
+  if (*window < 0) *sinks = 0;
+  if (*sinks > N) *sinks = N;
+  return FA_OK;
+}
+
+int check_strides(const long long* q, const long long* k, const long long* v, int B, int H, int Hk,
+                  int N, int d) {
+  Strides s;
+  int rc = read_strides(q, B, H, N, d, &s);
+  if (rc == FA_OK) rc = read_strides(k, B, Hk, N, d, &s);
+  return rc == FA_OK ? read_strides(v, B, Hk, N, d, &s) : rc;
+}
+
+int encode_rows(CUtensorMap* map, const void* ptr, const long long* strides, int dtype, int d,
+                int N, int H, int B) {
+  Strides s;
+  const int rc = read_strides(strides, B, H, N, d, &s);
+  if (rc != FA_OK) return rc;
+  return encode_cached(map, ptr, dtype, d, N, H, B, s.n, s.h, s.b, 128);
+}
+
+template <int HD, int ELT>
+int launch_fwd_sinks(const FwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
+  constexpr int QS = Pick<HD, ELT>::QS, KVS = Pick<HD, ELT>::KVS;
+  using C = FwdCfg<HD, QS, KVS, ELT>;
+  auto kernel = fa_fwd_kernel<HD, QS, KVS, ELT, false, true>;
+  const int slot = (HD == 64 ? 0 : HD == 128 ? 1 : 2) * 2 + (ELT == kBF16 ? 1 : 0);
+  const int rc = ensure_smem_attr(g_sinks[dev].fwd_attr[slot], kernel, C::SMEM_BYTES);
+  if (rc != FA_OK) return rc;
+  const int grid = p.num_tiles < st.sm_count ? p.num_tiles : st.sm_count;
+  kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// How the dK/dV kernel splits a sink block's query blocks: into pieces about
+// as long as the other key blocks' share of a head (window + 2 blocks), at
+// most so many that the pieces of all sink blocks hold no more sums than the
+// head has key blocks.
+void sink_pieces(int N, int window, int sinks, int* sink_blocks, int* pieces, int* piece_blocks) {
+  const int nblk = (N + 127) / 128;
+  *sink_blocks = window < 0 ? 0 : (sinks + 127) / 128;
+  *pieces = 1;
+  *piece_blocks = nblk;
+  if (*sink_blocks == 0) return;
+  const int share = (window + 127) / 128 + 2;
+  int want = (nblk + share - 1) / share;
+  if (want > nblk / *sink_blocks) want = nblk / *sink_blocks;
+  if (want <= 1) return;
+  *piece_blocks = (nblk + want - 1) / want;
+  *pieces = (nblk + *piece_blocks - 1) / *piece_blocks;
+}
+
+long long sink_part_floats(int B, int Hk, int d, int sink_blocks, int pieces) {
+  return pieces > 1 ? (long long)B * Hk * sink_blocks * pieces * 2 * 128 * d : 0;
+}
+
+template <int HD, bool BF16, bool KV>
+int launch_bwd_sinks_kernel(const BwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
+  using C = BwdCfg<HD, KV>;
+  auto kernel = fa_bwd_kernel<HD, BF16, KV, true>;
+  const int slot = (HD == 64 ? 0 : 4) + (BF16 ? 2 : 0) + (KV ? 1 : 0);
+  const int rc = ensure_smem_attr(g_sinks[dev].bwd_attr[slot], kernel, C::SMEM_BYTES);
+  if (rc != FA_OK) return rc;
+  const int grid = p.units < st.sm_count ? p.units : st.sm_count;
+  kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int HD, bool BF16>
+int launch_bwd_sinks(BwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
+  const int Hk = p.H / p.group;
+  const long long rows = (long long)p.B * p.H * p.N;
+  constexpr long long kRowsPerBlock = 256 / (HD / 8);  // bwd_dsum_kernel: HD / 8 threads a row
+  bwd_dsum_kernel<HD, BF16><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0,
+                              stream>>>(p.o, p.dout, p.dsum, rows);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  p.units = p.B * Hk * (p.sink_blocks * p.pieces + p.nblk - p.sink_blocks);
+  int rc = launch_bwd_sinks_kernel<HD, BF16, true>(p, st, dev, stream);
+  if (rc != FA_OK) return rc;
+  if (p.pieces > 1) {
+    const long long n = (long long)p.B * Hk * p.sink_blocks * 2 * 128 * (HD / 4);
+    sinks_sum_kernel<HD, BF16><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  p.units = p.B * p.H * p.nblk;
+  return launch_bwd_sinks_kernel<HD, BF16, false>(p, st, dev, stream);
+}
+
 }  // namespace
 
 extern "C" {
+
+int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                 const long long* q_strides, const long long* k_strides,
+                 const long long* v_strides, int B, int H, int Hk, int N, int d, int window,
+                 int sinks, float scale, int dtype, struct CUstream_st* stream) {
+  if (!q || !k || !v || !o) return FA_ERR_ARG;
+  int rc = check_sinks(B, H, Hk, N, d, &scale, &window, &sinks, dtype);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse))
+    return FA_ERR_ALIGN;
+  if ((rc = check_strides(q_strides, k_strides, v_strides, B, H, Hk, N, d)) != FA_OK) return rc;
+  if ((rc = get_encode_fn()) != FA_OK) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_o, o, nullptr, dtype, d, N, H, B)) != FA_OK)
+    return rc;
+  p.o = o;
+  p.lse = lse;
+  p.o_stride_n = d;
+  p.o_stride_h = (long long)N * d;
+  p.o_stride_b = (long long)H * N * d;
+  p.lse_stride_b = (long long)H * N;
+  p.lse_stride_h = N;
+  p.B = B, p.H = H, p.N = N, p.rows_total = N;
+  p.causal = 1;
+  p.window_left = window;
+  p.window_right = 0;
+  p.sinks = sinks;
+  p.group = H / Hk;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.o_scale = 1.f;
+  p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  const int rows_per_tile = 128 * q_tiles_for(d);
+  p.num_qblocks = (N + rows_per_tile - 1) / rows_per_tile;
+  p.num_tiles = B * H * p.num_qblocks;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == FA_BF16;
+  switch (d) {
+    case 64: return bf16 ? launch_fwd_sinks<64, kBF16>(p, *st, dev, s) : launch_fwd_sinks<64, kF16>(p, *st, dev, s);
+    case 128: return bf16 ? launch_fwd_sinks<128, kBF16>(p, *st, dev, s) : launch_fwd_sinks<128, kF16>(p, *st, dev, s);
+    default: return bf16 ? launch_fwd_sinks<256, kBF16>(p, *st, dev, s) : launch_fwd_sinks<256, kF16>(p, *st, dev, s);
+  }
+}
+
+long long fa_bwd_sinks_workspace(int B, int H, int Hk, int N, int d, int window, int sinks) {
+  float scale = 0.f;
+  int rc = check_sinks(B, H, Hk, N, d, &scale, &window, &sinks, FA_BF16);
+  if (rc == FA_OK && d > 128) rc = FA_ERR_HEADDIM;
+  if (rc != FA_OK) return rc;
+  int sink_blocks, pieces, piece_blocks;
+  sink_pieces(N, window, sinks, &sink_blocks, &pieces, &piece_blocks);
+  return sink_part_floats(B, Hk, d, sink_blocks, pieces) + (long long)B * H * N;
+}
+
+int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                 const void* dout, void* dq, void* dk, void* dv, const long long* q_strides,
+                 const long long* k_strides, const long long* v_strides, float* workspace, int B,
+                 int H, int Hk, int N, int d, int window, int sinks, float scale, int dtype,
+                 struct CUstream_st* stream) {
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace) return FA_ERR_ARG;
+  int rc = check_sinks(B, H, Hk, N, d, &scale, &window, &sinks, dtype);
+  if (rc != FA_OK) return rc;
+  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
+  for (const void* t : {q, k, v, o, dout, static_cast<const void*>(dq),
+                        static_cast<const void*>(dk), static_cast<const void*>(dv)})
+    if (!aligned16(t)) return FA_ERR_ALIGN;
+  if (!aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0) return FA_ERR_ALIGN;
+  if ((rc = check_strides(q_strides, k_strides, v_strides, B, H, Hk, N, d)) != FA_OK) return rc;
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.nblk = (N + 127) / 128;
+  sink_pieces(N, window, sinks, &p.sink_blocks, &p.pieces, &p.piece_blocks);
+  if ((long long)B * H * p.nblk > 0x7fffffffLL ||
+      (long long)B * Hk * (p.sink_blocks * (long long)p.pieces + p.nblk) > 0x7fffffffLL)
+    return FA_ERR_ARG;
+  if ((rc = get_encode_fn()) != FA_OK) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
+  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_do, dout, nullptr, dtype, d, N, H, B)) != FA_OK)
+    return rc;
+  p.o = o;
+  p.dout = dout;
+  p.lse = lse;
+  p.parts = workspace;
+  p.dsum = workspace + sink_part_floats(B, Hk, d, p.sink_blocks, p.pieces);
+  p.dq = dq, p.dk = dk, p.dv = dv;
+  p.out_vec32 = ((reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk) |
+                  reinterpret_cast<uintptr_t>(dv)) & 31u) == 0;
+  p.B = B, p.H = H, p.N = N;
+  p.causal = 1;
+  p.window = window, p.sinks = sinks, p.group = H / Hk;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == FA_BF16;
+  if (d == 64)
+    return bf16 ? launch_bwd_sinks<64, true>(p, *st, dev, s) : launch_bwd_sinks<64, false>(p, *st, dev, s);
+  return bf16 ? launch_bwd_sinks<128, true>(p, *st, dev, s) : launch_bwd_sinks<128, false>(p, *st, dev, s);
+}
 
 int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
                     const long long* q_strides, const long long* k_strides,

@@ -44,6 +44,9 @@ SIGNATURES = {
                     _VP]),
     "fa_bwd_noalloc": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I,
                             _I, _VP]),
+    "fa_fwd_sinks": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _VP, _VP] + [_I] * 7 + [_F, _I, _VP]),
+    "fa_bwd_sinks": (_I, [_VP, _VP, _VP, _VP, _FP] + [_VP] * 7 + [_FP] + [_I] * 7 + [_F, _I, _VP]),
+    "fa_bwd_sinks_workspace": (ctypes.c_longlong, [_I] * 7),
     "fa_qk_norm_rope": (_I, [_VP] * 11 + [_I, _VP, _VP, _I, _F] + [_I] * 8 + [_VP]),
     "fa_qk_norm_rope_bwd": (_I, [_VP] * 15 + [_I, _VP, _VP, _I, _F, _FP] + [_I] * 8 + [_VP]),
     "fa_rope_table": (_I, [_FP, _FP, _I, _I, ctypes.c_double, _I, ctypes.c_double, _I, _VP]),
@@ -400,6 +403,93 @@ def _weights(q_weight, k_weight, d, dtype):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _check_qkv(q, k, v):
+    """Checks of [B, H, N, d] queries against [B, Hk, N, d] keys and values."""
+    _check_rows(q, "q")
+    _check_rows(k, "k", q.dtype)
+    _check_rows(v, "v", q.dtype)
+    B, H, N, d = q.shape
+    if k.shape != v.shape or k.shape != (B, k.shape[1], N, d) or k.shape[1] < 1 \
+            or H % k.shape[1] != 0:
+        raise ValueError("k and v must be [B, Hk, N, d] with q's B, N and d, H a multiple of Hk")
+    return B, H, k.shape[1], N, d
+
+
+def _check_lse(lse, shape):
+    if not isinstance(lse, torch.Tensor) or lse.shape != shape or lse.dtype != torch.float32 \
+            or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous {list(shape)} float32 tensor")
+
+
+def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int,
+              scale: float | None = None, out: torch.Tensor | None = None,
+              lse: torch.Tensor | None = None, return_lse: bool = True):
+    """Causal attention over a sliding window plus the first ``sinks`` tokens,
+    which stay visible from every later query: key j is visible from query i iff
+    ``j <= i and (i - j <= window or j < sinks)`` (``window=-1``: plain causal).
+
+    ``q`` is ``[B, H, N, d]``, ``k`` and ``v`` ``[B, Hk, N, d]`` (each key head
+    shared by ``H / Hk`` query heads), of any strides with adjacent row elements.
+    Returns ``(O [B, H, N, d], LSE [B, H, N])``, contiguous; LSE is None when
+    ``return_lse`` is False."""
+    B, H, Hk, N, d = _check_qkv(q, k, v)
+    if out is None:
+        out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+    else:
+        _check_tensor(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q")
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
+    else:
+        _check_lse(lse, (B, H, N))
+    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("out", out),
+                                           ("lse", lse)) if t is not None])
+    with _on(dev):
+        rc = load().fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                 _ptr(lse), _strides(q), _strides(k), _strides(v), B, H, Hk, N, d,
+                                 int(window), int(sinks), 0.0 if scale is None else float(scale),
+                                 _DT[q.dtype], _stream_ptr(q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_sinks")
+    return out, lse
+
+
+def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+              lse: torch.Tensor, dout: torch.Tensor, window: int, sinks: int,
+              scale: float | None = None):
+    """Gradient of :func:`fwd_sinks` for an upstream gradient ``dout`` of its O:
+    ``(dq [B, H, N, d], dk, dv [B, Hk, N, d])``, contiguous; ``dk`` and ``dv``
+    are summed over the query heads that share a key head.  ``o``, ``lse``: the
+    forward's results; ``o`` and ``dout`` contiguous.  d is 64 or 128."""
+    B, H, Hk, N, d = _check_qkv(q, k, v)
+    for name, t in (("o", o), ("dout", dout)):
+        _check_tensor(t, name)
+        if t.shape != q.shape or t.dtype != q.dtype:
+            raise ValueError(f"{name} must match q")
+    _check_lse(lse, (B, H, N))
+    dev = same_device([("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse), ("dout", dout)])
+    lib = load()
+    floats = lib.fa_bwd_sinks_workspace(B, H, Hk, N, d, int(window), int(sinks))
+    if floats < 0:
+        raise FaError(int(floats), "fa_bwd_sinks_workspace")
+    dq = torch.empty((B, H, N, d), device=dev, dtype=q.dtype)
+    dk = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
+    dv = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
+    ws = torch.empty((floats,), device=dev, dtype=torch.float32)
+    with _on(dev):
+        rc = lib.fa_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                              lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                              dv.data_ptr(), _strides(q), _strides(k), _strides(v), ws.data_ptr(),
+                              B, H, Hk, N, d, int(window), int(sinks),
+                              0.0 if scale is None else float(scale), _DT[q.dtype], _stream_ptr(q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_bwd_sinks")
+    return dq, dk, dv
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",

@@ -243,6 +243,56 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
                    float scale, int causal, int dtype, struct CUstream_st *stream);
 
 /*
+ * Causal attention over a sliding window plus the sequence's first tokens
+ * ("sinks"), which stay visible from every later query, with key / value heads
+ * shared by groups of query heads:
+ *
+ *   key j is visible from query i iff j <= i and (i - j <= window or j < sinks)
+ *
+ *   q          : [B, H, N, d];  k, v : [B, Hk, N, d], H a multiple of Hk; query
+ *                head h reads key / value head h / (H / Hk)
+ *   *_strides  : host pointers to {batch, head, row} strides in elements, or
+ *                NULL for a contiguous tensor, as in fa_qk_norm_rope
+ *   o          : [B, H, N, d] contiguous (written)
+ *   lse        : [B, H, N] fp32 (written), or NULL
+ *   window     : >= 0, or -1: every earlier key is visible (plain causal)
+ *   sinks      : >= 0 (0: the window alone)
+ *   d          : 64, 128 or 256;  N <= 2^30
+ *   scale, dtype (FA_FP16 or FA_BF16), stream : as fa_fwd
+ *
+ * Every row sees its own key.  As in fa_fwd, all rows of q, k, v must hold
+ * finite values: a masked weight is zero, and zero times infinity is not.
+ * Key blocks that lie outside every row's view are neither loaded nor
+ * multiplied.
+ */
+int fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
+                 const long long *q_strides, const long long *k_strides,
+                 const long long *v_strides, int B, int H, int Hk, int N, int d, int window,
+                 int sinks, float scale, int dtype, struct CUstream_st *stream);
+
+/*
+ * Gradient of fa_fwd_sinks:
+ *
+ *   o, dout    : [B, H, N, d] contiguous;  lse : [B, H, N] (required); o and lse
+ *                as fa_fwd_sinks left them for the same arguments
+ *   dq         : [B, H, N, d] contiguous (written)
+ *   dk, dv     : [B, Hk, N, d] contiguous (written): summed over the query heads
+ *                that share the key / value head, in a fixed order
+ *   workspace  : fa_bwd_sinks_workspace(...) fp32, caller-owned scratch,
+ *                32-byte aligned
+ *   d          : 64 or 128
+ *   other arguments as fa_fwd_sinks.
+ */
+int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                 const void *dout, void *dq, void *dk, void *dv, const long long *q_strides,
+                 const long long *k_strides, const long long *v_strides, float *workspace, int B,
+                 int H, int Hk, int N, int d, int window, int sinks, float scale, int dtype,
+                 struct CUstream_st *stream);
+
+/* Floats of fa_bwd_sinks' workspace, or a negative status. */
+long long fa_bwd_sinks_workspace(int B, int H, int Hk, int N, int d, int window, int sinks);
+
+/*
  * RMS norm of every head's query and key and the rotation by position, in one
  * pass: what turns a projection's output into the q and k that fa_fwd takes.
  * For a row x of q (of k) at position p, weight w = q_weight (k_weight):

@@ -141,3 +141,114 @@ def test_overlapping_rows_are_recognised():
     assert fa._fresh_rows(x) and fa._fresh_rows(x.transpose(1, 2)) and fa._fresh_rows(x[:, :, ::2])
     assert not fa._fresh_rows(torch.zeros(1, 1, 5, 64).expand(2, 3, 5, 64))
     assert not fa._fresh_rows(torch.zeros(1000).as_strided((1, 1, 5, 64), (1000, 1000, 32, 1)))
+
+
+# --------------------------------------------------- window and sinks
+
+def test_visible_by_its_words():
+    m = layer.visible(7, 2, 1)
+    for i in range(7):
+        assert [j for j in range(7) if m[i, j]] == sorted({0} | set(range(max(0, i - 2), i + 1)))
+    assert (layer.visible(6, -1, 0) == np.tril(np.ones((6, 6), bool))).all()
+    assert (layer.visible(6, 0, 99) == np.tril(np.ones((6, 6), bool))).all()
+
+
+def test_sinks_gradient_against_differences():
+    B, H, Hk, N, d, W, A, sc = 1, 4, 2, 7, 4, 2, 1, 0.7
+    q, k, v, g = _rng(B, H, N, d, seed=1), _rng(B, Hk, N, d, seed=2), _rng(B, Hk, N, d, seed=3), \
+        _rng(B, H, N, d, seed=4)
+    grads, _ = layer.sinks_bwd(q, k, v, g, W, A, sc)
+    h = 1e-6
+    for n, (t, gr) in enumerate(zip((q, k, v), grads)):
+        for i in np.ndindex(t.shape):
+            args = [[x.copy() for x in (q, k, v)] for _ in range(2)]
+            args[0][n][i] += h
+            args[1][n][i] -= h
+            f = [(layer.sinks_fwd(*a, W, A, sc)[0] * g).sum() for a in args]
+            assert (f[0] - f[1]) / (2 * h) == pytest.approx(gr[i], abs=1e-7)
+
+
+def test_sinks_argument_errors(lib):
+    def fwd(q=P, o=P, lse=None, ks=None, B=1, H=4, Hk=2, N=300, d=128, W=64, A=4, scale=0.0, dtype=1):
+        return lib.fa_fwd_sinks(q, P, P, o, lse, None, ks, None, B, H, Hk, N, d, W, A, scale, dtype,
+                                None)
+
+    def bwd(q=P, dk=P, lse=P, ws=P, ks=None, B=1, H=4, Hk=2, N=300, d=128, W=64, A=4, scale=0.0, dtype=1):
+        return lib.fa_bwd_sinks(q, P, P, P, lse, P, P, dk, P, None, ks, None, ws, B, H, Hk, N, d, W,
+                                A, scale, dtype, None)
+    for call in (fwd, bwd):
+        for bad in (dict(q=None), dict(B=0), dict(H=0), dict(Hk=0), dict(Hk=3), dict(Hk=8), dict(N=0),
+                    dict(W=-2), dict(A=-1), dict(scale=-1.0), dict(scale=float("nan")),
+                    dict(N=(1 << 30) + 1), dict(ks=_strides(76800, 64, 256))):
+            assert call(**bad) == fa.FA_ERR_ARG, (call, bad)
+        assert call(d=96) == fa.FA_ERR_HEADDIM
+        for bad in (dict(dtype=2), dict(dtype=3)):
+            assert call(**bad) == fa.FA_ERR_DTYPE
+        for bad in (dict(q=P + 8), dict(lse=P + 2), dict(ks=_strides(76800, 38404, 128))):
+            assert call(**bad) == fa.FA_ERR_ALIGN, (call, bad)
+    assert fwd(o=None) == fa.FA_ERR_ARG
+    for bad in (dict(dk=None), dict(lse=None), dict(ws=None)):
+        assert bwd(**bad) == fa.FA_ERR_ARG
+    assert bwd(d=256) == fa.FA_ERR_HEADDIM
+    assert bwd(ws=P + 16) == fa.FA_ERR_ALIGN
+
+
+def test_sinks_workspace(lib):
+    w = lib.fa_bwd_sinks_workspace
+    assert w(2, 4, 2, 300, 128, -1, 4) == 2 * 4 * 300
+    assert w(2, 4, 2, 300, 128, 64, 0) == 2 * 4 * 300
+    # 32 blocks, shares of 4: one sink block in 8 pieces of [2, 128, d]
+    assert w(2, 4, 2, 4096, 64, 256, 4) == 2 * 4 * 4096 + 2 * 2 * 8 * 2 * 128 * 64
+    assert w(1, 4, 3, 300, 128, 64, 0) == fa.FA_ERR_ARG
+    assert w(1, 4, 2, 300, 256, 64, 0) == fa.FA_ERR_HEADDIM
+
+
+@pytest.mark.parametrize("N,window,sinks", [(1, -1, 0), (900, -1, 0), (900, 0, 0), (900, 0, 1),
+                                            (1000, 100, 4), (4096, 256, 4), (4096, 256, 300),
+                                            (3000, 130, 1500), (2049, 1, 128), (5000, 2047, 16)])
+def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks):
+    """The dK/dV and dQ kernels' units (fa_bwd_sm100.cuh sinks_unit, restated)
+    against the mask, by blocks: every visible pair of blocks once for each
+    query head, none twice."""
+    B, H, G = 1, 4, 2
+    Hk, nblk = H // G, (N + 127) // 128
+    W = -1 if window >= N - 1 else window
+    A = min(sinks, N) if W >= 0 else 0
+    ns = -(-A // 128)
+    pieces, size = 1, nblk
+    if ns:
+        want = min(-(-nblk // ((W + 127) // 128 + 2)), nblk // ns)
+        if want > 1:
+            size = -(-nblk // want)
+            pieces = -(-nblk // size)
+    pairs = []
+    for u in range(B * Hk * (ns * pieces + nblk - ns)):
+        rank, hk = divmod(u, B * Hk)
+        if rank < ns * pieces:
+            blk, piece = divmod(rank, pieces)
+            first = min(nblk, blk + piece * size)
+            end = min(nblk, first + size)
+        else:
+            blk = first = ns + rank - ns * pieces
+            end = nblk if W < 0 else min(nblk, (blk * 128 + 127 + W) // 128 + 1)
+        per = end - first
+        for it in range(per * G):
+            pairs.append((hk * G + it // per, first + it % per, blk))
+    dq = []
+    for u in range(B * H * nblk):
+        rank, h = divmod(u, B * H)
+        blk = nblk - 1 - rank
+        lo = 0 if W < 0 else max(0, blk * 128 - W) // 128
+        n = min(ns, blk + 1)
+        gap = max(n, lo)
+        count = blk + 1 - (gap - n)
+        assert count >= 1
+        dq += [(h, blk, it if it < n else it - n + gap) for it in range(count)]
+    m = layer.visible(N, W, A)
+    pad = np.zeros((nblk * 128, nblk * 128), bool)
+    pad[:N, :N] = m
+    need = {(h, i, j) for h in range(H) for i, j in
+            zip(*np.nonzero(pad.reshape(nblk, 128, nblk, 128).any((1, 3))))}
+    for got in (pairs, dq):
+        assert len(got) == len(set(got)) and need <= set(got)
+        assert len(got) <= len(need) + (H * ns * nblk if ns else 0)
