@@ -4,6 +4,7 @@
 // uses.
 #pragma once
 
+#include "fa_decode.cuh"
 #include "fa_rope.cuh"
 
 namespace {
@@ -243,9 +244,106 @@ int launch_bwd_sinks(BwdParams& p, DeviceState& st, int dev, cudaStream_t stream
   return launch_bwd_sinks_kernel<HD, BF16, false>(p, st, dev, stream);
 }
 
+// ------------------------------------------------------ one token at a time
+
+struct DecodeState {
+  std::atomic<bool> attr[10] = {};
+};
+DecodeState g_decode[kMaxDevices];
+
+template <int HD, int NT, bool BF16>
+int launch_decode(DecodeParams& p, int B, DeviceState& st, int dev, cudaStream_t stream) {
+  using C = DecodeCfg<HD, NT>;
+  auto kernel = decode_kernel<HD, NT, BF16>;
+  constexpr int slot = (HD == 64 ? 0 : HD == 128 ? 4 : 8) + (NT - 1) * 2 + (BF16 ? 1 : 0);
+  std::atomic<bool>& flag = g_decode[dev].attr[slot];
+  if (!flag.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return FA_ERR_CUDA;
+    }
+    const int rc = ensure_smem_attr(flag, kernel, C::SMEM_BYTES);
+    if (rc != FA_OK) return rc;
+  }
+  p.row_tiles = (p.group + C::Q - 1) / C::Q;
+  const long long tiles = (long long)B * p.Hk * p.row_tiles;
+  if (tiles > 65535) return FA_ERR_ARG;
+  // cluster size: enough CTAs for several on every SM, but no more warps than
+  // the longest view has steps
+  const long long most = p.window < 0 ? p.S : (long long)p.window + 1 + p.sinks;
+  const long long steps = ((most < p.S ? most : p.S) + 15) / 16;
+  int cl = 1;
+  while (cl < kDecodeMaxCluster && tiles * cl < 6ll * st.sm_count && 2 * cl * kDecodeWarps <= steps)
+    cl *= 2;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(cl, (unsigned)tiles);
+  cfg.blockDim = dim3(32 * kDecodeWarps);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cl;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+// Query heads a tile holds: 8, or 16 where a key head has more than 8 (its
+// keys are then read once for 16; at d = 256 the registers hold 8).
+template <bool BF16>
+int launch_decode_dims(DecodeParams& p, int B, int d, DeviceState& st, int dev, cudaStream_t s) {
+  if (d == 256) return launch_decode<256, 1, BF16>(p, B, st, dev, s);
+  if (d == 128)
+    return p.group > 8 ? launch_decode<128, 2, BF16>(p, B, st, dev, s)
+                       : launch_decode<128, 1, BF16>(p, B, st, dev, s);
+  return p.group > 8 ? launch_decode<64, 2, BF16>(p, B, st, dev, s)
+                     : launch_decode<64, 1, BF16>(p, B, st, dev, s);
+}
+
 }  // namespace
 
 extern "C" {
+
+int fa_decode_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                    const int* seqlens, const long long* k_strides, const long long* v_strides,
+                    int B, int H, int Hk, int S, int d, int window, int sinks, float scale,
+                    int dtype, struct CUstream_st* stream) {
+  if (!q || !k || !v || !o || !seqlens) return FA_ERR_ARG;
+  if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_HEADDIM;
+  if (B < 1 || H < 1 || Hk < 1 || S < 1 || H % Hk != 0 || S > 1 << 30) return FA_ERR_ARG;
+  if (window < -1 || sinks < 0) return FA_ERR_ARG;
+  if (!std::isfinite(scale) || scale < 0.f) return FA_ERR_ARG;
+  if (scale == 0.f) scale = 1.0f / std::sqrt(static_cast<float>(d));
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+      !aligned4(seqlens))
+    return FA_ERR_ALIGN;
+  if ((long long)B * H > 0x7fffffffLL) return FA_ERR_ARG;
+  Strides ks, vs;
+  int rc = read_strides(k_strides, B, Hk, S, d, &ks);
+  if (rc == FA_OK) rc = read_strides(v_strides, B, Hk, S, d, &vs);
+  if (rc != FA_OK) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
+  DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse, p.seqlens = seqlens;
+  p.kb = ks.b, p.kh = ks.h, p.kn = ks.n, p.vb = vs.b, p.vh = vs.h, p.vn = vs.n;
+  p.H = H, p.Hk = Hk, p.S = S, p.window = window, p.sinks = sinks, p.group = H / Hk;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == FA_BF16 ? launch_decode_dims<true>(p, B, d, *st, dev, s)
+                          : launch_decode_dims<false>(p, B, d, *st, dev, s);
+}
 
 int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
                  const long long* q_strides, const long long* k_strides,

@@ -47,6 +47,7 @@ SIGNATURES = {
     "fa_fwd_sinks": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _VP, _VP] + [_I] * 7 + [_F, _I, _VP]),
     "fa_bwd_sinks": (_I, [_VP, _VP, _VP, _VP, _FP] + [_VP] * 7 + [_FP] + [_I] * 7 + [_F, _I, _VP]),
     "fa_bwd_sinks_workspace": (ctypes.c_longlong, [_I] * 7),
+    "fa_decode_sinks": (_I, [_VP, _VP, _VP, _VP, _FP, _VP, _VP, _VP] + [_I] * 7 + [_F, _I, _VP]),
     "fa_qk_norm_rope": (_I, [_VP] * 11 + [_I, _VP, _VP, _I, _F] + [_I] * 8 + [_VP]),
     "fa_qk_norm_rope_bwd": (_I, [_VP] * 15 + [_I, _VP, _VP, _I, _F, _FP] + [_I] * 8 + [_VP]),
     "fa_rope_table": (_I, [_FP, _FP, _I, _I, ctypes.c_double, _I, ctypes.c_double, _I, _VP]),
@@ -490,6 +491,46 @@ def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_sinks")
     return dq, dk, dv
+
+
+def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: torch.Tensor,
+                 window: int, sinks: int, scale: float | None = None,
+                 out: torch.Tensor | None = None, return_lse: bool = True):
+    """:func:`fwd_sinks` one token at a time: ``q`` ``[B, H, d]`` holds each
+    sequence's newest query, ``k`` and ``v`` ``[B, Hk, S, d]`` (any strides with
+    adjacent row elements) its cached keys and values, of which the first
+    ``seqlens[b]`` (int32 ``[B]``, the newest token included) are in use.
+    Returns ``(O [B, H, d], LSE [B, H])``; a length of 0 gives O = 0 and LSE =
+    -inf.  Cache rows that are not visible are not read."""
+    _check_tensor(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, d]")
+    B, H, d = q.shape
+    _check_rows(k, "k", q.dtype)
+    _check_rows(v, "v", q.dtype)
+    Hk, S = k.shape[1], k.shape[2]
+    if k.shape != v.shape or k.shape != (B, Hk, S, d) or Hk < 1 or H % Hk != 0:
+        raise ValueError("k and v must be [B, Hk, S, d] with q's B and d, H a multiple of Hk")
+    if not isinstance(seqlens, torch.Tensor) or seqlens.dtype != torch.int32 \
+            or seqlens.shape != (B,) or not seqlens.is_contiguous():
+        raise ValueError("seqlens must be a contiguous int32 [B] tensor")
+    if out is None:
+        out = torch.empty((B, H, d), device=q.device, dtype=q.dtype)
+    else:
+        _check_tensor(out, "out")
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q")
+    lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if return_lse else None
+    dev = same_device([("q", q), ("k", k), ("v", v), ("seqlens", seqlens), ("out", out)])
+    with _on(dev):
+        rc = load().fa_decode_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                    _ptr(lse), seqlens.data_ptr(), _strides(k), _strides(v), B, H,
+                                    Hk, S, d, int(window), int(sinks),
+                                    0.0 if scale is None else float(scale), _DT[q.dtype],
+                                    _stream_ptr(q))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_sinks")
+    return out, lse
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",

@@ -289,6 +289,32 @@ int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, con
                  int H, int Hk, int N, int d, int window, int sinks, float scale, int dtype,
                  struct CUstream_st *stream);
 
+/*
+ * The attention of fa_fwd_sinks one token at a time: one query per sequence,
+ * its newest token, against a cache of that sequence's keys and values (the
+ * token's own among them).  With n = seqlens[b], row j of the cache is visible
+ * iff j < n and (j >= n - 1 - window or j < sinks).
+ *
+ *   q, o       : [B, H, d] contiguous;  lse : [B, H] fp32, or NULL
+ *   k, v       : caches [B, Hk, S, d] of the given strides (as fa_fwd_sinks: also
+ *                [B, S, Hk, d] by its strides), read only; rows that are not visible
+ *                are not read and may hold anything
+ *   seqlens    : [B] int32 on the device, 0 .. S.  n = 0 gives O = 0 and LSE =
+ *                -infinity.  A length out of range leaves the sequence's rows of o
+ *                and lse unwritten, and fa_device_status() returns FA_ERR_SEQLENS.
+ *   window     : >= 0, or -1 (every cached key);  sinks : >= 0
+ *   d          : 64, 128 or 256;  S <= 2^30;  scale as fa_fwd
+ *   size       : at most 65535 tiles, B * Hk * ceil(H / Hk / 8), else FA_ERR_ARG (16
+ *                in place of 8 where H / Hk > 8 and d < 256)
+ *
+ * A cache that keeps only the sinks and the newest keys (in any order) is
+ * read with window = -1.  Deterministic; one launch, no scratch.
+ */
+int fa_decode_sinks(const void *q, const void *k, const void *v, void *o, float *lse,
+                    const int *seqlens, const long long *k_strides, const long long *v_strides,
+                    int B, int H, int Hk, int S, int d, int window, int sinks, float scale,
+                    int dtype, struct CUstream_st *stream);
+
 /* Floats of fa_bwd_sinks' workspace, or a negative status. */
 long long fa_bwd_sinks_workspace(int B, int H, int Hk, int N, int d, int window, int sinks);
 
@@ -382,7 +408,7 @@ const char *fa_strerror(int status);
  * Reads (and, if clear != 0, resets) the current device's watchdog word.
  * Synchronises the current device first.  Returns FA_OK, FA_ERR_TIMEOUT when a
  * kernel gave up on a bounded wait, FA_ERR_SEQLENS when fa_fwd_varlen met
- * offsets out of range, FA_ERR_POSITIONS when fa_qk_norm_rope met a position
+ * offsets or fa_decode_sinks a length out of range, FA_ERR_POSITIONS when fa_qk_norm_rope met a position
  * outside its table (`*detail`, if not NULL, receives the (role << 8) | site
  * code), or FA_ERR_CUDA.
  */

@@ -252,3 +252,35 @@ def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks):
     for got in (pairs, dq):
         assert len(got) == len(set(got)) and need <= set(got)
         assert len(got) <= len(need) + (H * ns * nblk if ns else 0)
+
+
+def test_decode_reference_is_the_last_row():
+    q, k, v = _rng(1, 4, 9, 8, seed=1), _rng(1, 2, 9, 8, seed=2), _rng(1, 2, 9, 8, seed=3)
+    o, lse = layer.sinks_fwd(q, k, v, 3, 2, 0.5)
+    o1, lse1, _ = layer.sinks_decode(q[:, :, -1], k, v, [9], 3, 2, 0.5)
+    assert np.allclose(o[:, :, -1], o1) and np.allclose(lse[:, :, -1], lse1)
+
+
+def test_decode_argument_errors(lib):
+    def call(q=P, o=P, lse=None, lens=P, ks=None, vs=None, B=2, H=8, Hk=2, S=300, d=128, W=64, A=4,
+             scale=0.0, dtype=1):
+        return lib.fa_decode_sinks(q, P, P, o, lse, lens, ks, vs, B, H, Hk, S, d, W, A, scale, dtype,
+                                   None)
+    for bad in (dict(q=None), dict(o=None), dict(lens=None), dict(B=0), dict(H=0), dict(Hk=0), dict(Hk=3),
+                dict(S=0), dict(S=(1 << 30) + 1), dict(W=-2), dict(A=-1), dict(scale=-1.0),
+                dict(scale=float("inf")), dict(ks=_strides(76800, 64, 128)),
+                dict(vs=_strides(1 << 46, 38400, 128), B=3), dict(B=1 << 20, H=1 << 12, Hk=1 << 12)):
+        assert call(**bad) == fa.FA_ERR_ARG, bad
+    assert call(d=80) == fa.FA_ERR_HEADDIM
+    for bad in (dict(dtype=2), dict(dtype=3)):
+        assert call(**bad) == fa.FA_ERR_DTYPE
+    for bad in (dict(q=P + 8), dict(lse=P + 2), dict(lens=P + 1), dict(vs=_strides(76800, 38400, 132))):
+        assert call(**bad) == fa.FA_ERR_ALIGN, bad
+
+
+def test_python_sinks_refusals():
+    x = torch.zeros(1, 2, 8, 64, dtype=torch.float16)
+    for call in (lambda: fa.fwd_sinks(x, x, x, 4, 1), lambda: fa.bwd_sinks(x, x, x, x, x, x, 4, 1),
+                 lambda: fa.decode_sinks(x[:, :, 0], x, x, torch.zeros(1, dtype=torch.int32), 4, 1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
