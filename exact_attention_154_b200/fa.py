@@ -8,6 +8,7 @@ sm_100 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -359,9 +360,43 @@ def _check_rows(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be [B, H, N, d] with adjacent elements in a row")
 
 
+@functools.lru_cache(maxsize=256)
+def _stride_array(b, h, n):
+    return (ctypes.c_longlong * 3)(b, h, n)
+
+
 def _strides(t: torch.Tensor):
     """The (batch, head, row) strides argument of the C ABI; None when contiguous."""
-    return None if t.is_contiguous() else (ctypes.c_longlong * 3)(*t.stride()[:3])
+    return None if t.is_contiguous() else _stride_array(*t.stride()[:3])
+
+
+def _launch(what: str, dev: torch.device, named, args):
+    """Calls entry point ``what`` with ``args`` and the current stream of ``dev``,
+    with that device current; ``named`` are the call's tensors (or None), which
+    must all live on it.  Raises what the library refuses."""
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    fn = getattr(load(), what)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with _on(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != FA_OK:
+        raise FaError(rc, what)
+
+
+def _new_like(t: torch.Tensor):
+    """A new contiguous tensor of ``t``'s shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _check_out(t: torch.Tensor, name: str, like: torch.Tensor):
+    """A given output: its input's shape and type, rows that do not overlap."""
+    _check_rows(t, name, like.dtype)
+    if t.shape != like.shape or not _fresh_rows(t):
+        raise ValueError(f"{name} must have its input's shape and rows that do not overlap")
 
 
 def _fresh_rows(t: torch.Tensor):
@@ -437,7 +472,7 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
     ``return_lse`` is False."""
     B, H, Hk, N, d = _check_qkv(q, k, v)
     if out is None:
-        out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+        out = _new_like(q)
     else:
         _check_tensor(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype:
@@ -448,15 +483,10 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
         lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
     else:
         _check_lse(lse, (B, H, N))
-    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("out", out),
-                                           ("lse", lse)) if t is not None])
-    with _on(dev):
-        rc = load().fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 _ptr(lse), _strides(q), _strides(k), _strides(v), B, H, Hk, N, d,
-                                 int(window), int(sinks), 0.0 if scale is None else float(scale),
-                                 _DT[q.dtype], _stream_ptr(q))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fwd_sinks")
+    _launch("fa_fwd_sinks", q.device, (("k", k), ("v", v), ("out", out), ("lse", lse)),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _strides(q),
+             _strides(k), _strides(v), B, H, Hk, N, d, int(window), int(sinks),
+             0.0 if scale is None else float(scale), _DT[q.dtype]))
     return out, lse
 
 
@@ -473,23 +503,17 @@ def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor
         if t.shape != q.shape or t.dtype != q.dtype:
             raise ValueError(f"{name} must match q")
     _check_lse(lse, (B, H, N))
-    dev = same_device([("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse), ("dout", dout)])
-    lib = load()
-    floats = lib.fa_bwd_sinks_workspace(B, H, Hk, N, d, int(window), int(sinks))
+    floats = load().fa_bwd_sinks_workspace(B, H, Hk, N, d, int(window), int(sinks))
     if floats < 0:
         raise FaError(int(floats), "fa_bwd_sinks_workspace")
-    dq = torch.empty((B, H, N, d), device=dev, dtype=q.dtype)
-    dk = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
-    dv = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
-    ws = torch.empty((floats,), device=dev, dtype=torch.float32)
-    with _on(dev):
-        rc = lib.fa_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                              lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                              dv.data_ptr(), _strides(q), _strides(k), _strides(v), ws.data_ptr(),
-                              B, H, Hk, N, d, int(window), int(sinks),
-                              0.0 if scale is None else float(scale), _DT[q.dtype], _stream_ptr(q))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_bwd_sinks")
+    dq, dk, dv = _new_like(q), _new_like(k), _new_like(v)
+    ws = lse.new_empty((floats,))
+    _launch("fa_bwd_sinks", q.device,
+            (("k", k), ("v", v), ("o", o), ("lse", lse), ("dout", dout)),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+             dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _strides(q),
+             _strides(k), _strides(v), ws.data_ptr(), B, H, Hk, N, d, int(window), int(sinks),
+             0.0 if scale is None else float(scale), _DT[q.dtype]))
     return dq, dk, dv
 
 
@@ -515,21 +539,16 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
             or seqlens.shape != (B,) or not seqlens.is_contiguous():
         raise ValueError("seqlens must be a contiguous int32 [B] tensor")
     if out is None:
-        out = torch.empty((B, H, d), device=q.device, dtype=q.dtype)
+        out = torch.empty_like(q)
     else:
         _check_tensor(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must match q")
     lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if return_lse else None
-    dev = same_device([("q", q), ("k", k), ("v", v), ("seqlens", seqlens), ("out", out)])
-    with _on(dev):
-        rc = load().fa_decode_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                    _ptr(lse), seqlens.data_ptr(), _strides(k), _strides(v), B, H,
-                                    Hk, S, d, int(window), int(sinks),
-                                    0.0 if scale is None else float(scale), _DT[q.dtype],
-                                    _stream_ptr(q))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_decode_sinks")
+    _launch("fa_decode_sinks", q.device, (("k", k), ("v", v), ("seqlens", seqlens), ("out", out)),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
+             seqlens.data_ptr(), _strides(k), _strides(v), B, H, Hk, S, d, int(window), int(sinks),
+             0.0 if scale is None else float(scale), _DT[q.dtype]))
     return out, lse
 
 
@@ -550,12 +569,9 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "no
         raise ValueError("max_pos and rot must be positive")
     cos = torch.empty((max_pos, rot // 2), device=dev, dtype=torch.float32)
     sin = torch.empty_like(cos)
-    with _on(cos.device):
-        rc = load().fa_rope_table(cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base),
-                                  ROPE_SCALING[scaling], float(factor), int(original_max_pos),
-                                  _stream_ptr(cos))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_rope_table")
+    _launch("fa_rope_table", cos.device, (),
+            (cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base), ROPE_SCALING[scaling],
+             float(factor), int(original_max_pos)))
     return cos, sin
 
 
@@ -582,25 +598,20 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch
     max_pos, rot = _table(cos, sin, positions, B, N)
     wt = _weights(q_weight, k_weight, d, q.dtype)
     if q_out is None:
-        q_out = torch.empty((B, H, N, d), device=q.device, dtype=q.dtype)
+        q_out = _new_like(q)
+    else:
+        _check_out(q_out, "q_out", q)
     if k_out is None:
-        k_out = torch.empty((B, Hk, N, d), device=q.device, dtype=q.dtype)
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        _check_rows(t, name, q.dtype)
-        if t.shape != like.shape or not _fresh_rows(t):
-            raise ValueError(f"{name} must have its input's shape and rows that do not overlap")
-    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("cos", cos), ("sin", sin),
-                                           ("positions", positions), ("q_weight", q_weight),
-                                           ("k_weight", k_weight), ("q_out", q_out),
-                                           ("k_out", k_out)) if t is not None])
-    with _on(dev):
-        rc = load().fa_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _strides(q),
-            _strides(k), _strides(q_out), _strides(k_out), cos.data_ptr(), sin.data_ptr(),
-            _ptr(positions), max_pos, _ptr(q_weight), _ptr(k_weight), wt, float(eps), B, H, Hk, N,
-            d, rot, int(bool(interleaved)), _DT[q.dtype], _stream_ptr(q))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_qk_norm_rope")
+        k_out = _new_like(k)
+    else:
+        _check_out(k_out, "k_out", k)
+    _launch("fa_qk_norm_rope", q.device,
+            (("k", k), ("cos", cos), ("sin", sin), ("positions", positions),
+             ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out), ("k_out", k_out)),
+            (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _strides(q),
+             _strides(k), _strides(q_out), _strides(k_out), cos.data_ptr(), sin.data_ptr(),
+             _ptr(positions), max_pos, _ptr(q_weight), _ptr(k_weight), wt, float(eps), B, H, Hk, N,
+             d, rot, int(bool(interleaved)), _DT[q.dtype]))
     return q_out, k_out
 
 
@@ -622,24 +633,18 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
             raise ValueError(f"{name} does not match q and k")
     max_pos, rot = _table(cos, sin, positions, B, N)
     wt = _weights(q_weight, k_weight, d, q.dtype)
-    dev = same_device([(n, t) for n, t in (("q", q), ("k", k), ("dq_out", dq_out),
-                                           ("dk_out", dk_out), ("cos", cos), ("sin", sin),
-                                           ("positions", positions), ("q_weight", q_weight),
-                                           ("k_weight", k_weight)) if t is not None])
-    dq = torch.empty((B, H, N, d), device=dev, dtype=q.dtype)
-    dk = torch.empty((B, Hk, N, d), device=dev, dtype=q.dtype)
+    dq, dk = _new_like(q), _new_like(k)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = torch.empty((NORM_ROPE_PARTS, 2, d), device=dev, dtype=torch.float32)
-    with _on(dev):
-        rc = load().fa_qk_norm_rope_bwd(
-            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), _ptr(dqw), _ptr(dkw), _strides(dq_out), _strides(dk_out), _strides(q),
-            _strides(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions), max_pos, _ptr(q_weight),
-            _ptr(k_weight), wt, float(eps), ws.data_ptr(), B, H, Hk, N, d, rot,
-            int(bool(interleaved)), _DT[q.dtype], _stream_ptr(q))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_qk_norm_rope_bwd")
+    ws = cos.new_empty((NORM_ROPE_PARTS, 2, d))
+    _launch("fa_qk_norm_rope_bwd", q.device,
+            (("k", k), ("dq_out", dq_out), ("dk_out", dk_out), ("cos", cos), ("sin", sin),
+             ("positions", positions), ("q_weight", q_weight), ("k_weight", k_weight)),
+            (dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+             dk.data_ptr(), _ptr(dqw), _ptr(dkw), _strides(dq_out), _strides(dk_out), _strides(q),
+             _strides(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions), max_pos, _ptr(q_weight),
+             _ptr(k_weight), wt, float(eps), ws.data_ptr(), B, H, Hk, N, d, rot,
+             int(bool(interleaved)), _DT[q.dtype]))
     return dq, dk, dqw, dkw
 
 
