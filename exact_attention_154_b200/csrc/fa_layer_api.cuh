@@ -56,23 +56,33 @@ template <int HD, bool BF16, bool INTER, bool BWD>
 int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   constexpr int kTokens = 32 / (HD / 8), kWarps = kRopeThreads / 32;
   const int HT = p.op[0].heads + p.op[1].heads;
-  const long long groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
+  p.groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
   // heads a warp walks over: more of them share the loaded cos / sin, fewer
   // give a small call more warps
   int hpw = 1;
-  while (hpw < 8 && hpw < HT && groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
+  while (hpw < 8 && hpw < HT && p.groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
     hpw *= 2;
   p.heads_per_warp = hpw;
-  p.chunks = (HT + hpw - 1) / hpw;
-  p.items = groups * p.chunks;
-  const long long ctas = (p.items + kWarps - 1) / kWarps;
+  // CTAs in proportion to q's and k's items; the gradient's leave a row of
+  // partial sums each
+  long long ctas[2];
+  for (int i = 0; i < 2; ++i) {
+    p.chunks[i] = (p.op[i].heads + hpw - 1) / hpw;
+    ctas[i] = (p.groups * p.chunks[i] + kWarps - 1) / kWarps;
+  }
   const long long most = BWD ? FA_NORM_ROPE_PARTS : 1 << 20;
-  const int grid = (int)(ctas < most ? ctas : most);
+  if (ctas[0] + ctas[1] > most) {
+    const long long k = most * p.op[1].heads / HT;
+    ctas[1] = k < 1 ? 1 : k > most - 1 ? most - 1 : k;
+    ctas[0] = most - ctas[1];
+  }
+  p.ctas_q = (int)ctas[0];
+  const int grid = (int)(ctas[0] + ctas[1]);
   qk_norm_rope_kernel<HD, BF16, INTER, BWD><<<grid, kRopeThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (BWD && (p.op[0].w != nullptr || p.op[1].w != nullptr)) {
-    norm_weight_sum_kernel<BF16><<<2 * d / 32, 256, 0, stream>>>(p.parts, grid, d, p.op[0].dw,
-                                                                p.op[1].dw, p.w_fp32);
+    norm_weight_sum_kernel<BF16><<<dim3(d / 32, 2), 1024, 0, stream>>>(
+        p.parts, p.ctas_q, grid, d, p.op[0].dw, p.op[1].dw, p.w_fp32);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
@@ -269,12 +279,15 @@ int launch_decode(DecodeParams& p, int B, DeviceState& st, int dev, cudaStream_t
   p.row_tiles = (p.group + C::Q - 1) / C::Q;
   const long long tiles = (long long)B * p.Hk * p.row_tiles;
   if (tiles > 65535) return FA_ERR_ARG;
-  // cluster size: enough CTAs for several on every SM, but no more warps than
-  // the longest view has steps
+  // Cluster size: two CTAs for every SM and no more (measured at 128 tiles of
+  // 8192 keys: 2 CTAs a tile 78 us, 1: 84, 4: 86, 8: 85; at 32 tiles 8: 26 us,
+  // 4: 28, 16: 44), and at least one step for every second warp (one tile pair
+  // of 17 steps: 8 CTAs 6.0 us, 16: 6.6, 4: 6.7).
   const long long most = p.window < 0 ? p.S : (long long)p.window + 1 + p.sinks;
-  const long long steps = ((most < p.S ? most : p.S) + 15) / 16;
+  const long long steps = ((most < p.S ? most : p.S) + C::KEYS - 1) / C::KEYS;
   int cl = 1;
-  while (cl < kDecodeMaxCluster && tiles * cl < 6ll * st.sm_count && 2 * cl * kDecodeWarps <= steps)
+  while (cl < kDecodeMaxCluster && tiles * 2 * cl <= 2ll * st.sm_count &&
+         2 * cl * kDecodeWarps <= 2 * steps)
     cl *= 2;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
@@ -331,15 +344,20 @@ int fa_decode_sinks(const void* q, const void* k, const void* v, void* o, float*
   int rc = read_strides(k_strides, B, Hk, S, d, &ks);
   if (rc == FA_OK) rc = read_strides(v_strides, B, Hk, S, d, &vs);
   if (rc != FA_OK) return rc;
+  if ((rc = get_encode_fn()) != FA_OK) return rc;
   DeviceState* st = nullptr;
   int dev = 0;
   if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
   DecodeParams p;
   std::memset(&p, 0, sizeof(p));
-  p.q = q, p.k = k, p.v = v, p.o = o, p.lse = lse, p.seqlens = seqlens;
-  p.kb = ks.b, p.kh = ks.h, p.kn = ks.n, p.vb = vs.b, p.vh = vs.h, p.vn = vs.n;
+  p.q = q, p.o = o, p.lse = lse, p.seqlens = seqlens;
+  const int keys = d == 256 ? DecodeCfg<256, 1>::KEYS : DecodeCfg<128, 1>::KEYS;  // of a step
+  if ((rc = encode_cached(&p.tmap_k, k, dtype, d, S, Hk, B, ks.n, ks.h, ks.b, keys)) != FA_OK ||
+      (rc = encode_cached(&p.tmap_v, v, dtype, d, S, Hk, B, vs.n, vs.h, vs.b, keys)) != FA_OK)
+    return rc;
   p.H = H, p.Hk = Hk, p.S = S, p.window = window, p.sinks = sinks, p.group = H / Hk;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == FA_BF16 ? launch_decode_dims<true>(p, B, d, *st, dev, s)
                           : launch_decode_dims<false>(p, B, d, *st, dev, s);

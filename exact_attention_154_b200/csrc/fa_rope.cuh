@@ -16,11 +16,12 @@
 // The statistics and both sums are fp32; each result is rounded once.
 //
 // What bounds it: memory.  Every row is read once and written once (the
-// gradient reads two), there is no reuse to tile for.  d / 8 lanes hold a row
-// in 16-byte pieces, so a warp's access covers whole rows; the two halves of
-// a pair sit in different lanes when the pairs are (i, i + rot/2) and are
-// exchanged by shuffles.  A warp keeps its tokens' cos / sin in registers and
-// walks over heads, several rows in flight.
+// gradient reads two), there is no reuse to tile for.  d / 8 lanes hold a row,
+// each two pieces of four columns chosen so that it holds whole pairs (columns
+// 4 l and rot/2 + 4 l on, or 8 l on when interleaved): no exchange between
+// lanes but the row's sum, and a warp's accesses still cover whole rows.  A
+// warp keeps its tokens' four cos / sin values in registers and walks over
+// heads of one operand, several rows in flight.
 #pragma once
 
 #include "fa_fwd_sm100.cuh"
@@ -46,18 +47,20 @@ struct RopeParams {
   const float* cos;   // [max_pos, rot / 2]
   const float* sin;
   const int* positions;  // [B, N], or nullptr: the row index
-  float* parts;          // gradient: [gridDim.x][2][d] sums of g * n
+  float* parts;          // gradient: [gridDim.x][d] sums of g * n
   int B, N, max_pos, rot, w_fp32;
   float eps;
-  int heads_per_warp, chunks;  // head chunks of the q and k heads together
-  long long items;             // token groups x chunks
+  int heads_per_warp;
+  int chunks[2];       // head chunks of q and of k
+  int ctas_q;          // CTAs that take q's items; the rest take k's
+  long long groups;    // token groups
 };
 
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+  const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     float2 p;
     if constexpr (BF16)
       p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
@@ -68,69 +71,33 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]),
-                    pack2<BF16>(f[6], f[7]));
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  return make_uint2(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]));
 }
 
-// Eight consecutive weights as fp32, from the operands' type or from fp32.
+// Four consecutive weights as fp32, from the operands' type or from fp32.
 template <bool BF16>
-__device__ __forceinline__ void load_weight8(const void* w, int w_fp32, int e0, float (&f)[8]) {
+__device__ __forceinline__ void load_weight4(const void* w, int w_fp32, int e, float* f) {
   if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+    f[0] = f[1] = f[2] = f[3] = 1.f;
   } else if (w_fp32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + e0);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + e));
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   } else {
-    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + e0)), f);
+    unpack4<BF16>(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + e)), f);
   }
 }
 
-// cos / sin of a lane's eight columns e0 .. e0 + 7 of the rotated part.  Half
-// layout: one value a column (the columns lie in one half, rot / 2 being a
-// multiple of 8), sin negated in the first half, so that
-// out = y * cos + partner * sin.  Interleaved: the four pairs' values twice.
+// Turns a lane's four pairs: (x[i], x[4 + i]), or (x[2i], x[2i + 1]).
 template <bool INTER>
-__device__ __forceinline__ void load_angles(const float* cos, const float* sin, long long row,
-                                            int half, int e0, float (&c)[8], float (&s)[8]) {
-  if constexpr (INTER) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(cos + row * half + e0 / 2));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(sin + row * half + e0 / 2));
-    const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[2 * i] = c[2 * i + 1] = ca[i];
-      s[2 * i] = -sa[i];
-      s[2 * i + 1] = sa[i];
-    }
-  } else {
-    const bool second = e0 >= half;
-    const long long at = row * half + (second ? e0 - half : e0);
-    const float4* pc = reinterpret_cast<const float4*>(cos + at);
-    const float4* ps = reinterpret_cast<const float4*>(sin + at);
-    const float4 a = __ldg(pc), b = __ldg(pc + 1), u = __ldg(ps), v = __ldg(ps + 1);
-    const float sg = second ? 1.f : -1.f;
-    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
-    s[0] = sg * u.x, s[1] = sg * u.y, s[2] = sg * u.z, s[3] = sg * u.w;
-    s[4] = sg * v.x, s[5] = sg * v.y, s[6] = sg * v.z, s[7] = sg * v.w;
-  }
-}
-
-// Turns a lane's eight columns; `partner` is the lane holding the other
-// halves of its pairs (half layout).  Every lane of the warp takes part.
-template <bool INTER>
-__device__ __forceinline__ void rotate8(float (&y)[8], const float (&c)[8], const float (&s)[8],
-                                        bool turned, int partner) {
-  float o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o[i] = INTER ? y[i ^ 1] : __shfl_sync(0xffffffffu, y[i], partner);
-  if (turned) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i], c[i], o[i] * s[i]);
+  for (int i = 0; i < 4; ++i) {
+    float& a = x[INTER ? 2 * i : i];
+    float& b = x[INTER ? 2 * i + 1 : 4 + i];
+    const float u = a * c[i] - b * s[i];
+    b = fmaf(a, s[i], b * c[i]);
+    a = u;
   }
 }
 
@@ -144,33 +111,42 @@ __device__ __forceinline__ float row_sum(float v) {
 
 constexpr int kRopeThreads = 256;
 
-// One warp item: 32 / (HD / 8) tokens x up to heads_per_warp of the q and k
-// heads.  BWD: turns the arriving gradient back and takes it through the
-// norm; each CTA sums its rows' g * n and leaves the sums in `parts`.
+// One warp item: 32 / (HD / 8) tokens x up to heads_per_warp heads of q or k.
+// BWD: turns the arriving gradient back and takes it through the norm; each
+// CTA sums its rows' g * n and leaves the sums in `parts`.
 template <int HD, bool BF16, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3)
+    qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = HD / 8;         // lanes of a row
   constexpr int TOKENS = 32 / LANES;    // tokens of a warp item
   constexpr int WARPS = kRopeThreads / 32;
-  constexpr int U = BWD ? 2 : 4;        // rows in flight
+  constexpr int U = 4;                  // rows in flight
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sub = lane % LANES, e0 = sub * 8;
+  const int sub = lane % LANES;
   const int half = p.rot / 2;
-  const bool turned = e0 < p.rot;
-  // half layout: column e pairs with e + rot/2, rot / 16 lanes further
-  const int partner = turned ? (e0 < half ? lane + p.rot / 16 : lane - p.rot / 16) : lane;
-  const int HT = p.op[0].heads + p.op[1].heads;
+  // this lane's columns: ea .. ea + 3 and eb .. eb + 3
+  const bool turned = 8 * sub < p.rot;
+  const int ea = !INTER && turned ? 4 * sub : 8 * sub;
+  const int eb = !INTER && turned ? half + 4 * sub : 8 * sub + 4;
+  const bool is_k = static_cast<int>(blockIdx.x) >= p.ctas_q;
+  const RopeOperand& op = p.op[is_k];
+  const int cta = is_k ? blockIdx.x - p.ctas_q : blockIdx.x;
+  const int ctas = is_k ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int chunks = p.chunks[is_k];
+  const bool normed = op.w != nullptr;
   const long long tokens = static_cast<long long>(p.B) * p.N;
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weight8<BF16>(p.op[0].w, p.w_fp32, e0, wq);
-  load_weight8<BF16>(p.op[1].w, p.w_fp32, e0, wk);
+  const long long items = p.groups * chunks;
+  float w[8], dw[8];
+  load_weight4<BF16>(op.w, p.w_fp32, ea, w);
+  load_weight4<BF16>(op.w, p.w_fp32, eb, w + 4);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
 
-  for (long long item = static_cast<long long>(blockIdx.x) * WARPS + warp; item < p.items;
-       item += static_cast<long long>(gridDim.x) * WARPS) {
-    const long long group = item / p.chunks;
-    const int chunk = static_cast<int>(item - group * p.chunks);
+  for (long long item = static_cast<long long>(cta) * WARPS + warp; item < items;
+       item += static_cast<long long>(ctas) * WARPS) {
+    const long long group = item / chunks;
+    const int h_begin = static_cast<int>(item - group * chunks) * p.heads_per_warp;
+    const int h_end = min(op.heads, h_begin + p.heads_per_warp);
     const long long token = group * TOKENS + lane / LANES;
     bool live = token < tokens;
     const int b = live ? static_cast<int>(token / p.N) : 0;
@@ -182,42 +158,43 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
       if (sub == 0) atomicCAS(&g_fa_watchdog, 0u, (kRoleArgs << 8) | kSitePositions);
       live = false;
     }
-    float c[8], s[8];
-    if (turned) {
-      load_angles<INTER>(p.cos, p.sin, live ? pos : 0, half, e0, c, s);
-      if constexpr (BWD) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = -s[i];
-      }
+    const uint16_t* x_row = static_cast<const uint16_t*>(op.x) + b * op.xb + n * op.xn;
+    const uint16_t* g_row = static_cast<const uint16_t*>(op.g) + b * op.gb + n * op.gn;
+    uint16_t* y_row = static_cast<uint16_t*>(op.y) + b * op.yb + n * op.yn;
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (turned && live) {
+      const long long at = static_cast<long long>(pos) * half + 4 * sub;
+      const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + at));
+      const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + at));
+      const float sg = BWD ? -1.f : 1.f;  // the gradient turns back
+      c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+      s[0] = sg * sv.x, s[1] = sg * sv.y, s[2] = sg * sv.z, s[3] = sg * sv.w;
     }
-    const int h_end = min(HT, (chunk + 1) * p.heads_per_warp);
-    for (int h0 = chunk * p.heads_per_warp; h0 < h_end; h0 += U) {
-      uint4 xv[U], gv[U];
-      const bool normed0 = p.op[0].w != nullptr, normed1 = p.op[1].w != nullptr;
+#pragma unroll 1
+    for (int h0 = h_begin; h0 < h_end; h0 += U) {
+      uint2 xv[U][2], gv[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        xv[u] = gv[u] = make_uint4(0u, 0u, 0u, 0u);
-        const int hh = h0 + u;
-        if (live && hh < h_end) {
-          const bool is_k = hh >= p.op[0].heads;
-          const RopeOperand& o = p.op[is_k];
-          const int h = is_k ? hh - p.op[0].heads : hh;
-          if (!BWD || (is_k ? normed1 : normed0))
-            xv[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.x) + b * o.xb +
-                                                    h * o.xh + n * o.xn + e0);
-          if constexpr (BWD)
-            gv[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o.g) + b * o.gb +
-                                                    h * o.gh + n * o.gn + e0);
+        xv[u][0] = xv[u][1] = gv[u][0] = gv[u][1] = make_uint2(0u, 0u);
+        if (live && h0 + u < h_end) {
+          if (!BWD || normed) {
+            const uint16_t* x = x_row + (h0 + u) * op.xh;
+            xv[u][0] = *reinterpret_cast<const uint2*>(x + ea);
+            xv[u][1] = *reinterpret_cast<const uint2*>(x + eb);
+          }
+          if constexpr (BWD) {
+            const uint16_t* g = g_row + (h0 + u) * op.gh;
+            gv[u][0] = *reinterpret_cast<const uint2*>(g + ea);
+            gv[u][1] = *reinterpret_cast<const uint2*>(g + eb);
+          }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int hh = h0 + u;
-        if (hh >= h_end) break;
-        const bool is_k = hh >= p.op[0].heads;
-        const bool normed = is_k ? normed1 : normed0;
+        if (h0 + u >= h_end) break;
         float x[8], y[8];
-        unpack8<BF16>(xv[u], x);
+        unpack4<BF16>(xv[u][0], x);
+        unpack4<BF16>(xv[u][1], x + 4);
         float r = 1.f;
         if (normed) {
           float ss = 0.f;
@@ -228,21 +205,19 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
         }
         if constexpr (!BWD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i] * r * (is_k ? wk[i] : wq[i]);
-          rotate8<INTER>(y, c, s, turned, partner);
+          for (int i = 0; i < 8; ++i) y[i] = x[i] * r * w[i];
+          rotate<INTER>(y, c, s);
         } else {
-          unpack8<BF16>(gv[u], y);
-          rotate8<INTER>(y, c, s, turned, partner);
+          unpack4<BF16>(gv[u][0], y);
+          unpack4<BF16>(gv[u][1], y + 4);
+          rotate<INTER>(y, c, s);
           if (normed) {
             float dot = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               x[i] *= r;  // n
-              if (is_k)
-                dwk[i] = fmaf(y[i], x[i], dwk[i]);
-              else
-                dwq[i] = fmaf(y[i], x[i], dwq[i]);
-              y[i] *= is_k ? wk[i] : wq[i];
+              dw[i] = fmaf(y[i], x[i], dw[i]);
+              y[i] *= w[i];
               dot = fmaf(y[i], x[i], dot);
             }
             dot = row_sum<LANES>(dot) * (1.f / HD);
@@ -251,68 +226,63 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopePa
           }
         }
         if (live) {
-          const RopeOperand& o = p.op[is_k];
-          const int h = is_k ? hh - p.op[0].heads : hh;
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.y) + b * o.yb + h * o.yh + n * o.yn +
-                                    e0) = pack8<BF16>(y);
+          uint16_t* out = y_row + (h0 + u) * op.yh;
+          *reinterpret_cast<uint2*>(out + ea) = pack4<BF16>(y);
+          *reinterpret_cast<uint2*>(out + eb) = pack4<BF16>(y + 4);
         }
       }
     }
   }
   if constexpr (BWD) {
+    if (!normed) return;
     // the CTA's sums: lanes of different tokens, then the warps in order
-    __shared__ float sums[WARPS][2][HD];
+    __shared__ float sums[WARPS][HD];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
-      for (int sh = LANES; sh < 32; sh <<= 1) {
-        dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], sh);
-        dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], sh);
-      }
-      if (lane < LANES) {
-        sums[warp][0][e0 + i] = dwq[i];
-        sums[warp][1][e0 + i] = dwk[i];
-      }
+      for (int sh = LANES; sh < 32; sh <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], sh);
+      if (lane < LANES) sums[warp][(i < 4 ? ea : eb - 4) + i] = dw[i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * HD; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < HD; i += kRopeThreads) {
       float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) t += (&sums[w][0][0])[i];
-      p.parts[static_cast<long long>(blockIdx.x) * 2 * HD + i] = t;
+      for (int v = 0; v < WARPS; ++v) t += sums[v][i];
+      p.parts[static_cast<long long>(blockIdx.x) * HD + i] = t;
     }
   }
 }
 
-// dw of q and k: the CTAs' sums added in a fixed order (32 columns a block,
-// eight warps over the parts, then the warps in order), rounded to the
-// weight's type.
+// dw of q (blockIdx.y 0) and k (1): the sums of the operand's CTAs added in a
+// fixed order (32 columns a block, 32 warps over the parts, then the warps in
+// order), rounded to the weight's type.
 template <bool BF16>
-__global__ void __launch_bounds__(256) norm_weight_sum_kernel(const float* __restrict__ parts,
-                                                              int nparts, int d, void* dq, void* dk,
-                                                              int w_fp32) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __restrict__ parts,
+                                                               int ctas_q, int ctas, int d, void* dq,
+                                                               void* dk, int w_fp32) {
+  __shared__ float sums[32][33];
+  void* out = blockIdx.y == 0 ? dq : dk;
+  if (out == nullptr) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int col = blockIdx.x * 32 + lane;  // of the 2 d columns (q, then k)
+  const int col = blockIdx.x * 32 + lane;
+  const int first = blockIdx.y == 0 ? 0 : ctas_q, end = blockIdx.y == 0 ? ctas_q : ctas;
   float t = 0.f;
 #pragma unroll 8
-  for (int i = warp; i < nparts; i += 8) t += parts[static_cast<long long>(i) * 2 * d + col];
+  for (int i = first + warp; i < end; i += 32) t += parts[static_cast<long long>(i) * d + col];
   sums[warp][lane] = t;
   __syncthreads();
-  if (warp == 0) {
-    t = 0.f;
+  // warp w sums column w's 32 partial sums, lane by lane in tree order
+  t = sums[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sums[w][lane];
-    void* out = col < d ? dq : dk;
-    if (out != nullptr) {
-      const int e = col < d ? col : col - d;
-      if (w_fp32)
-        static_cast<float*>(out)[e] = t;
-      else if (BF16)
-        static_cast<__nv_bfloat16*>(out)[e] = __float2bfloat16_rn(t);
-      else
-        static_cast<__half*>(out)[e] = __float2half_rn(t);
-    }
+  for (int sh = 16; sh > 0; sh >>= 1) t += __shfl_xor_sync(0xffffffffu, t, sh);
+  if (lane == 0) {
+    const int e = blockIdx.x * 32 + warp;
+    if (w_fp32)
+      static_cast<float*>(out)[e] = t;
+    else if (BF16)
+      static_cast<__nv_bfloat16*>(out)[e] = __float2bfloat16_rn(t);
+    else
+      static_cast<__half*>(out)[e] = __float2half_rn(t);
   }
 }
 

@@ -525,7 +525,7 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
     adjacent row elements) its cached keys and values, of which the first
     ``seqlens[b]`` (int32 ``[B]``, the newest token included) are in use.
     Returns ``(O [B, H, d], LSE [B, H])``; a length of 0 gives O = 0 and LSE =
-    -inf.  Cache rows that are not visible are not read."""
+    -inf.  Cache rows that are not visible may hold anything."""
     _check_tensor(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, H, d]")
@@ -636,7 +636,7 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     dq, dk = _new_like(q), _new_like(k)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = cos.new_empty((NORM_ROPE_PARTS, 2, d))
+    ws = cos.new_empty((NORM_ROPE_PARTS, d))
     _launch("fa_qk_norm_rope_bwd", q.device,
             (("k", k), ("dq_out", dq_out), ("dk_out", dk_out), ("cos", cos), ("sin", sin),
              ("positions", positions), ("q_weight", q_weight), ("k_weight", k_weight)),

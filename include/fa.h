@@ -67,7 +67,7 @@ enum fa_dtype { FA_FP16 = 0, FA_BF16 = 1, FA_E4M3 = 2, FA_FP32 = 3 };
 /* How fa_rope_table scales the rotation for contexts longer than trained on. */
 enum fa_rope_scaling { FA_ROPE_PLAIN = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_YARN = 3 };
 
-/* fa_qk_norm_rope_bwd: rows of [2, d] fp32 its workspace holds. */
+/* fa_qk_norm_rope_bwd: rows of d fp32 its workspace holds. */
 enum { FA_NORM_ROPE_PARTS = 592 };
 
 /*
@@ -298,7 +298,7 @@ int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, con
  *   q, o       : [B, H, d] contiguous;  lse : [B, H] fp32, or NULL
  *   k, v       : caches [B, Hk, S, d] of the given strides (as fa_fwd_sinks: also
  *                [B, S, Hk, d] by its strides), read only; rows that are not visible
- *                are not read and may hold anything
+ *                may hold anything
  *   seqlens    : [B] int32 on the device, 0 .. S.  n = 0 gives O = 0 and LSE =
  *                -infinity.  A length out of range leaves the sequence's rows of o
  *                and lse unwritten, and fa_device_status() returns FA_ERR_SEQLENS.
@@ -367,7 +367,7 @@ int fa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
  *                dq_out and dk_out themselves when those are contiguous
  *   dq_weight, dk_weight : [d] of type `weight_dtype` (written), required where
  *                the weight is given
- *   workspace  : FA_NORM_ROPE_PARTS * 2 * d fp32, caller-owned scratch
+ *   workspace  : FA_NORM_ROPE_PARTS * d fp32, caller-owned scratch
  *   other arguments as fa_qk_norm_rope.
  *
  * The weights' gradients are summed in fp32 in an order that does not change
