@@ -56,11 +56,12 @@ template <int HD, bool BF16, bool INTER, bool BWD>
 int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   constexpr int kTokens = 32 / (HD / 8), kWarps = kRopeThreads / 32;
   const int HT = p.op[0].heads + p.op[1].heads;
-  p.groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
+  const long long groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
+  p.blocks = (int)((groups + kWarps - 1) / kWarps);
   // heads a warp walks over: more of them share the loaded cos / sin, fewer
   // give a small call more warps
   int hpw = 1;
-  while (hpw < 8 && hpw < HT && p.groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
+  while (hpw < 16 && hpw < HT && groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
     hpw *= 2;
   p.heads_per_warp = hpw;
   // CTAs in proportion to q's and k's items; the gradient's leave a row of
@@ -68,7 +69,8 @@ int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   long long ctas[2];
   for (int i = 0; i < 2; ++i) {
     p.chunks[i] = (p.op[i].heads + hpw - 1) / hpw;
-    ctas[i] = (p.groups * p.chunks[i] + kWarps - 1) / kWarps;
+    ctas[i] = (long long)p.blocks * p.chunks[i];
+    if (ctas[i] > 1 << 30) return FA_ERR_ARG;
   }
   const long long most = BWD ? FA_NORM_ROPE_PARTS : 1 << 20;
   if (ctas[0] + ctas[1] > most) {

@@ -51,54 +51,47 @@ struct RopeParams {
   int B, N, max_pos, rot, w_fp32;
   float eps;
   int heads_per_warp;
-  int chunks[2];       // head chunks of q and of k
-  int ctas_q;          // CTAs that take q's items; the rest take k's
-  long long groups;    // token groups
+  int chunks[2];  // head chunks of q and of k
+  int ctas_q;     // CTAs that take q's items; the rest take k's
+  int blocks;     // blocks of a CTA's tokens (one token group a warp)
 };
 
+// Four 16-bit values as two pairs of fp32, and back.
 template <bool BF16>
-__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+__device__ __forceinline__ void unpack4(const uint2& v, float2* f) {
   const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float2 p;
     if constexpr (BF16)
-      p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      f[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
     else
-      p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
+      f[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
   }
 }
 template <bool BF16>
-__device__ __forceinline__ uint2 pack4(const float* f) {
-  return make_uint2(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]));
+__device__ __forceinline__ uint2 pack4(const float2* f) {
+  return make_uint2(pack2<BF16>(f[0].x, f[0].y), pack2<BF16>(f[1].x, f[1].y));
 }
 
 // Four consecutive weights as fp32, from the operands' type or from fp32.
 template <bool BF16>
-__device__ __forceinline__ void load_weight4(const void* w, int w_fp32, int e, float* f) {
+__device__ __forceinline__ void load_weight4(const void* w, int w_fp32, int e, float2* f) {
   if (w == nullptr) {
-    f[0] = f[1] = f[2] = f[3] = 1.f;
+    f[0] = f[1] = make_float2(1.f, 1.f);
   } else if (w_fp32) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + e));
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
   } else {
     unpack4<BF16>(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + e)), f);
   }
 }
 
-// Turns a lane's four pairs: (x[i], x[4 + i]), or (x[2i], x[2i + 1]).
+// The other halves of the pairs that register pair k of a lane's eight columns
+// belongs to: the same places of the other piece, or its own two swapped.
 template <bool INTER>
-__device__ __forceinline__ void rotate(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float& a = x[INTER ? 2 * i : i];
-    float& b = x[INTER ? 2 * i + 1 : 4 + i];
-    const float u = a * c[i] - b * s[i];
-    b = fmaf(a, s[i], b * c[i]);
-    a = u;
-  }
+__device__ __forceinline__ float2 partner(const float2 (&x)[4], int k) {
+  if constexpr (INTER) return make_float2(x[k].y, x[k].x);
+  return x[k ^ 2];
 }
 
 // Sum over the LANES lanes of a row.
@@ -108,19 +101,28 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int sh = LANES / 2; sh > 0; sh >>= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
   return v;
 }
+template <int LANES>
+__device__ __forceinline__ float row_dot(const float2 (&x)[4], const float2 (&y)[4]) {
+  float2 t = __fmul2_rn(x[0], y[0]);
+#pragma unroll
+  for (int k = 1; k < 4; ++k) t = __ffma2_rn(x[k], y[k], t);
+  return row_sum<LANES>(t.x + t.y);
+}
 
 constexpr int kRopeThreads = 256;
 
-// One warp item: 32 / (HD / 8) tokens x up to heads_per_warp heads of q or k.
+// A CTA's item: up to heads_per_warp heads of q or k x one group of 32 / (HD / 8)
+// tokens for each warp.  Lanes without a token compute its last one again and
+// write nothing.
 // BWD: turns the arriving gradient back and takes it through the norm; each
 // CTA sums its rows' g * n and leaves the sums in `parts`.
 template <int HD, bool BF16, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = HD / 8;         // lanes of a row
   constexpr int TOKENS = 32 / LANES;    // tokens of a warp item
   constexpr int WARPS = kRopeThreads / 32;
-  constexpr int U = 4;                  // rows in flight
+  constexpr int U = BWD ? 1 : 2;        // rows in work; as many more are on their way
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int sub = lane % LANES;
   const int half = p.rot / 2;
@@ -134,103 +136,140 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3)
   const int ctas = is_k ? gridDim.x - p.ctas_q : p.ctas_q;
   const int chunks = p.chunks[is_k];
   const bool normed = op.w != nullptr;
-  const long long tokens = static_cast<long long>(p.B) * p.N;
-  const long long items = p.groups * chunks;
-  float w[8], dw[8];
+  const int tokens = p.B * p.N;
+  const int items = p.blocks * chunks;
+  float2 w[4], dw[4];
   load_weight4<BF16>(op.w, p.w_fp32, ea, w);
-  load_weight4<BF16>(op.w, p.w_fp32, eb, w + 4);
+  load_weight4<BF16>(op.w, p.w_fp32, eb, w + 2);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  for (int k = 0; k < 4; ++k) dw[k] = make_float2(0.f, 0.f);
 
-  for (long long item = static_cast<long long>(cta) * WARPS + warp; item < items;
-       item += static_cast<long long>(ctas) * WARPS) {
-    const long long group = item / chunks;
-    const int h_begin = static_cast<int>(item - group * chunks) * p.heads_per_warp;
-    const int h_end = min(op.heads, h_begin + p.heads_per_warp);
-    const long long token = group * TOKENS + lane / LANES;
-    bool live = token < tokens;
-    const int b = live ? static_cast<int>(token / p.N) : 0;
-    const int n = live ? static_cast<int>(token - static_cast<long long>(b) * p.N) : 0;
+#pragma unroll 1
+  for (int item = cta; item < items; item += ctas) {
+    const int block = item / chunks;
+    const int h_begin = (item - block * chunks) * p.heads_per_warp;
+    const int heads = min(op.heads - h_begin, p.heads_per_warp);
+    const long long at_token = static_cast<long long>(block) * (WARPS * TOKENS) + warp * TOKENS + lane / LANES;
+    bool live = at_token < tokens;
+    const int token = live ? static_cast<int>(at_token) : tokens - 1;
+    const int b = token / p.N, n = token - b * p.N;
+    const uint16_t* x_at = static_cast<const uint16_t*>(op.x) + b * op.xb + h_begin * op.xh + n * op.xn;
+    const uint16_t* g_at = static_cast<const uint16_t*>(op.g) + b * op.gb + h_begin * op.gh + n * op.gn;
+    uint16_t* y_at = static_cast<uint16_t*>(op.y) + b * op.yb + h_begin * op.yh + n * op.yn;
+    // the rows of heads h .. h + U - 1 of the chunk
+    auto load = [&](int h, uint2 (&x)[U][2], uint2 (&g)[U][2]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (h + u >= heads) break;
+        if (!BWD || normed) {
+          x[u][0] = *reinterpret_cast<const uint2*>(x_at + ea);
+          x[u][1] = *reinterpret_cast<const uint2*>(x_at + eb);
+          x_at += op.xh;
+        }
+        if constexpr (BWD) {
+          g[u][0] = *reinterpret_cast<const uint2*>(g_at + ea);
+          g[u][1] = *reinterpret_cast<const uint2*>(g_at + eb);
+          g_at += op.gh;
+        }
+      }
+    };
+    uint2 xv[U][2], gv[U][2];
+    load(0, xv, gv);  // before the position, which the cos / sin loads wait for
     int pos = n;
-    if (p.positions != nullptr && live) pos = __ldg(p.positions + token);
-    if (live && (pos < 0 || pos >= p.max_pos)) {
+    if (p.positions != nullptr) pos = __ldg(p.positions + token);
+    if (pos < 0 || pos >= p.max_pos) {
       // outside the table: the token's rows are left unwritten, and reported
       if (sub == 0) atomicCAS(&g_fa_watchdog, 0u, (kRoleArgs << 8) | kSitePositions);
       live = false;
+      pos = 0;
     }
-    const uint16_t* x_row = static_cast<const uint16_t*>(op.x) + b * op.xb + n * op.xn;
-    const uint16_t* g_row = static_cast<const uint16_t*>(op.g) + b * op.gb + n * op.gn;
-    uint16_t* y_row = static_cast<uint16_t*>(op.y) + b * op.yb + n * op.yn;
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (turned && live) {
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (turned) {
       const long long at = static_cast<long long>(pos) * half + 4 * sub;
       const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + at));
       const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + at));
-      const float sg = BWD ? -1.f : 1.f;  // the gradient turns back
       c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-      s[0] = sg * sv.x, s[1] = sg * sv.y, s[2] = sg * sv.z, s[3] = sg * sv.w;
+      sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+    }
+    // Forward: out = own * own_c + partner * other_c, the weights included
+    // (first of a pair: a cos - b sin; second: b cos + a sin).  The gradient
+    // turns back with c and sn as they are.
+    float2 own_c[4], other_c[4];
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (INTER) {
+          own_c[k] = make_float2(c[k], c[k]);
+          other_c[k] = make_float2(-sn[k], sn[k]);
+        } else {
+          const float sg = k < 2 ? -1.f : 1.f;
+          own_c[k] = make_float2(c[2 * (k % 2)], c[2 * (k % 2) + 1]);
+          other_c[k] = make_float2(sg * sn[2 * (k % 2)], sg * sn[2 * (k % 2) + 1]);
+        }
+        own_c[k] = __fmul2_rn(own_c[k], w[k]);
+        other_c[k] = __fmul2_rn(other_c[k], partner<INTER>(w, k));
+      }
     }
 #pragma unroll 1
-    for (int h0 = h_begin; h0 < h_end; h0 += U) {
-      uint2 xv[U][2], gv[U][2];
+    for (int h0 = 0; h0 < heads; h0 += U) {
+      uint2 xn[U][2], gn[U][2];
+      load(h0 + U, xn, gn);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        xv[u][0] = xv[u][1] = gv[u][0] = gv[u][1] = make_uint2(0u, 0u);
-        if (live && h0 + u < h_end) {
-          if (!BWD || normed) {
-            const uint16_t* x = x_row + (h0 + u) * op.xh;
-            xv[u][0] = *reinterpret_cast<const uint2*>(x + ea);
-            xv[u][1] = *reinterpret_cast<const uint2*>(x + eb);
-          }
-          if constexpr (BWD) {
-            const uint16_t* g = g_row + (h0 + u) * op.gh;
-            gv[u][0] = *reinterpret_cast<const uint2*>(g + ea);
-            gv[u][1] = *reinterpret_cast<const uint2*>(g + eb);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h0 + u >= h_end) break;
-        float x[8], y[8];
+        if (h0 + u >= heads) break;
+        float2 x[4], y[4], o[4];
         unpack4<BF16>(xv[u][0], x);
-        unpack4<BF16>(xv[u][1], x + 4);
-        float r = 1.f;
-        if (normed) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-          r = rsqrtf(row_sum<LANES>(ss) * (1.f / HD) + p.eps);
-          if (!live) r = 0.f;  // no row here: 0 * inf must not reach the sums
+        unpack4<BF16>(xv[u][1], x + 2);
+        if constexpr (BWD) {
+          unpack4<BF16>(gv[u][0], y);
+          unpack4<BF16>(gv[u][1], y + 2);
         }
         if constexpr (!BWD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i] * r * w[i];
-          rotate<INTER>(y, c, s);
+          for (int k = 0; k < 4; ++k)
+            o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(partner<INTER>(x, k), other_c[k]));
+        } else if constexpr (INTER) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = make_float2(y[k].x * c[k] + y[k].y * sn[k], y[k].y * c[k] - y[k].x * sn[k]);
         } else {
-          unpack4<BF16>(gv[u][0], y);
-          unpack4<BF16>(gv[u][1], y + 4);
-          rotate<INTER>(y, c, s);
-          if (normed) {
-            float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] *= r;  // n
-              dw[i] = fmaf(y[i], x[i], dw[i]);
-              y[i] *= w[i];
-              dot = fmaf(y[i], x[i], dot);
-            }
-            dot = row_sum<LANES>(dot) * (1.f / HD);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = r * fmaf(-x[i], dot, y[i]);
+          for (int k = 0; k < 2; ++k) {
+            o[k] = make_float2(y[k].x * c[2 * k] + y[k + 2].x * sn[2 * k],
+                               y[k].y * c[2 * k + 1] + y[k + 2].y * sn[2 * k + 1]);
+            o[k + 2] = make_float2(y[k + 2].x * c[2 * k] - y[k].x * sn[2 * k],
+                                   y[k + 2].y * c[2 * k + 1] - y[k].y * sn[2 * k + 1]);
           }
         }
+        if (normed) {
+          const float r = rsqrtf(row_dot<LANES>(x, x) * (1.f / HD) + p.eps);
+          const float2 rr = make_float2(r, r);
+          if constexpr (BWD) {
+            // o = g; n = x r; dn = g w; dx = r (dn - n mean(dn n))
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = __fmul2_rn(x[k], rr);
+              if (live) dw[k] = __ffma2_rn(o[k], x[k], dw[k]);
+              o[k] = __fmul2_rn(o[k], w[k]);
+            }
+            const float dot = row_dot<LANES>(o, x) * (-1.f / HD);
+            const float2 dd = make_float2(dot, dot);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = __ffma2_rn(x[k], dd, o[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = __fmul2_rn(o[k], rr);
+        }
         if (live) {
-          uint16_t* out = y_row + (h0 + u) * op.yh;
-          *reinterpret_cast<uint2*>(out + ea) = pack4<BF16>(y);
-          *reinterpret_cast<uint2*>(out + eb) = pack4<BF16>(y + 4);
+          *reinterpret_cast<uint2*>(y_at + ea) = pack4<BF16>(o);
+          *reinterpret_cast<uint2*>(y_at + eb) = pack4<BF16>(o + 2);
+          y_at += op.yh;
         }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) xv[u][i] = xn[u][i], gv[u][i] = gn[u][i];
     }
   }
   if constexpr (BWD) {
@@ -239,9 +278,10 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? 2 : 3)
     __shared__ float sums[WARPS][HD];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      float t = i & 1 ? dw[i / 2].y : dw[i / 2].x;
 #pragma unroll
-      for (int sh = LANES; sh < 32; sh <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], sh);
-      if (lane < LANES) sums[warp][(i < 4 ? ea : eb - 4) + i] = dw[i];
+      for (int sh = LANES; sh < 32; sh <<= 1) t += __shfl_xor_sync(0xffffffffu, t, sh);
+      if (lane < LANES) sums[warp][(i < 4 ? ea : eb - 4) + i] = t;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < HD; i += kRopeThreads) {
