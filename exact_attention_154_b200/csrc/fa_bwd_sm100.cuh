@@ -60,13 +60,6 @@ struct BwdParams {
   int units;            // B * H * nblk: one unit = one resident key (dK/dV) or query (dQ) block
   int out_vec32;        // dq, dk, dv 32-byte aligned: the epilogue writes whole 32-byte sectors
   unsigned long long wait_limit_ns;
-  // Kernels with SINKS only (causal): key j is visible from query i iff j <= i
-  // and (window < 0 or i - j <= window or j < sinks); query head h reads key /
-  // value head h / group, and dK, dV sum over the group.
-  int window, sinks, group;
-  int sink_blocks;      // key blocks holding sinks (0 when window < 0)
-  int pieces, piece_blocks;  // dK/dV of a sink block: pieces of that many query blocks
-  float* parts;         // pieces > 1: fp32 [B, H / group, sink_blocks, pieces, {dV, dK}, 128, d]
 };
 
 template <int HD, bool KV>
@@ -218,107 +211,19 @@ __device__ __forceinline__ void store_acc(void* dst_row, const uint32_t* acc, fl
   }
 }
 
-// Writes NC fp32 columns of row r of dV (a0) and dK (a1) of one piece of a
-// sink block to its partial sums.
-template <int NC>
-__device__ __forceinline__ void store_part(float* parts, long long part, int hd, int r, int c,
-                                           const uint32_t* a0, const uint32_t* a1) {
-  float* at = parts + (part * 2 * 128 + r) * hd + c;
-#pragma unroll
-  for (int i = 0; i < NC / 8; ++i) {
-    st_global_v8(at + 8 * i, a0 + 8 * i);
-    st_global_v8(at + 128ll * hd + 8 * i, a1 + 8 * i);
-  }
-}
-
 // One unit of work: a resident key block (dK/dV) or query block (dQ) of one
 // (b, h), and the streamed blocks it meets.
 struct BwdUnit {
   int bh, blk, b, h;
   int first, count;  // streamed blocks first .. first + count - 1
-  // SINKS.  dK/dV: the streamed query blocks first .. first + per_head - 1 of
-  // each query head h0 .. h0 + group - 1 in turn.  dQ: the streamed key blocks
-  // are 0 .. ns - 1, then gap_end on, of key head h0.
-  int h0, per_head, ns, gap_end;
-  long long part;    // dK/dV: index of this piece's partial sums, or -1
 };
-
-// Query blocks [first, end) of piece `piece` of sink block blk.
-__device__ __forceinline__ void sink_piece(const BwdParams& p, int blk, int piece, int* first,
-                                           int* end) {
-  *first = min(p.nblk, blk + piece * p.piece_blocks);
-  *end = min(p.nblk, *first + p.piece_blocks);
-}
-
-// SINKS: units with the most blocks first -- the sink blocks' pieces (every
-// later query sees a sink, so unsplit such a unit would outlast the others),
-// then the other key blocks from the front; for dQ the query blocks from the
-// back.
-__device__ __forceinline__ BwdUnit sinks_unit(const BwdParams& p, int u, bool kv) {
-  BwdUnit w;
-  const int Hk = p.H / p.group;
-  const int heads = kv ? p.B * Hk : p.B * p.H;
-  const int rank = u / heads;
-  w.bh = u - rank * heads;
-  w.b = w.bh / (kv ? Hk : p.H);
-  w.h = w.bh - w.b * (kv ? Hk : p.H);
-  w.part = -1;
-  if (kv) {
-    w.h0 = w.h * p.group;
-    w.ns = w.gap_end = 0;
-    int end;
-    const int split = p.sink_blocks * p.pieces;
-    if (rank < split) {
-      w.blk = rank / p.pieces;
-      const int piece = rank - w.blk * p.pieces;
-      sink_piece(p, w.blk, piece, &w.first, &end);
-      if (p.pieces > 1)
-        w.part = (static_cast<long long>(w.bh) * p.sink_blocks + w.blk) * p.pieces + piece;
-    } else {
-      w.blk = p.sink_blocks + rank - split;
-      w.first = w.blk;
-      // query blocks with a row at most `window` past the block's last key
-      end = p.window < 0 ? p.nblk
-                         : min(static_cast<long long>(p.nblk),
-                               (w.blk * 128ll + 127 + p.window) / 128 + 1);
-    }
-    w.per_head = end - w.first;
-    w.count = w.per_head * p.group;
-  } else {
-    w.blk = p.nblk - 1 - rank;
-    w.h0 = w.h / p.group;
-    const int lo = p.window < 0 ? 0 : max(0, w.blk * 128 - p.window) / 128;
-    w.ns = min(p.sink_blocks, w.blk + 1);
-    w.gap_end = max(w.ns, lo);
-    w.first = 0;
-    w.per_head = 0;
-    w.count = w.blk + 1 - (w.gap_end - w.ns);
-  }
-  return w;
-}
-
-// Head and block of a unit's streamed step.
-struct BwdStep {
-  int h, blk;
-};
-template <bool SINKS, bool KV>
-__device__ __forceinline__ BwdStep bwd_step(const BwdUnit& w, int it) {
-  if constexpr (!SINKS) return {w.h, w.first + it};
-  if constexpr (KV) {
-    const int g = it / w.per_head;
-    return {w.h0 + g, w.first + it - g * w.per_head};
-  }
-  return {w.h0, it < w.ns ? it : it - w.ns + w.gap_end};
-}
 
 // Units in the order they are handed out.  Non-causal: (b, h)-major, so the
 // units running at once share a head's streamed tiles in L2.  Causal: the
 // units with the most blocks first (key block 0 of every head for dK/dV, the
 // last query block for dQ), so that with the snake hand-out below the
 // persistent CTAs get equal work.
-template <bool SINKS>
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdParams& p, int u, bool kv) {
-  if constexpr (SINKS) return sinks_unit(p, u, kv);
   BwdUnit w;
   if (p.causal) {
     const int nbh = p.B * p.H;
@@ -350,7 +255,7 @@ __device__ __forceinline__ int bwd_unit_of(int round, int cta, int G) {
 // Persistent: min(units, SMs) CTAs, each taking units in turn; every role
 // counts the streamed steps over all its units, so ring slots and per-step
 // barrier phases run on across units.
-template <int HD, bool BF16, bool KV, bool SINKS = false>
+template <int HD, bool BF16, bool KV>
 __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<HD, KV>;
@@ -397,8 +302,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
       for (int round = 0; ok && round * G < p.units; ++round) {
         const int u = bwd_unit_of(round, cta, G);
         if (u >= p.units) continue;
-        const BwdUnit w = bwd_unit<SINKS>(p, u, KV);
-        if (SINKS && w.count <= 0) continue;  // a piece past the sequence's end
+        const BwdUnit w = bwd_unit(p, u, KV);
         // resident pair: K_j, V_j (dkdv) or Q_i, dO_i (dq), once the previous
         // unit's S and dP products have ended
         if (k > 0 && !(ok = wait_phase(bars + 8 * C::B_RES_EMPTY, (k - 1) & 1, abort_flag, lim,
@@ -413,8 +317,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
         // A_it then B_it, each into its ring once the slot's previous tile is
         // released
         for (int it = 0; ok && it < w.count; ++it) {
-          const BwdStep st = bwd_step<SINKS, KV>(w, it);
-          const int gs = g + it, row0 = st.blk * 128;
+          const int gs = g + it, row0 = (w.first + it) * 128;
 #pragma unroll 1
           for (int ring = 0; ring < 2; ++ring) {
             const int slots = ring ? C::B_SLOTS : C::A_SLOTS;
@@ -427,7 +330,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
             mbar_arrive_expect_tx(full, C::TILE_BYTES);
             load_tile<HD>(base + (ring ? C::RB_OFF : C::RA_OFF) + slot * C::TILE_BYTES,
                           ring ? (KV ? &p.tmap_do : &p.tmap_v) : (KV ? &p.tmap_q : &p.tmap_k),
-                          full, row0, st.h, w.b);
+                          full, row0, w.h, w.b);
             ++(ring ? issued_b : issued_a);
           }
         }
@@ -487,8 +390,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
       for (int round = 0; ok && round * G < p.units; ++round) {
         const int u = bwd_unit_of(round, cta, G);
         if (u >= p.units) continue;
-        const int count = bwd_unit<SINKS>(p, u, KV).count;
-        if (SINKS && count <= 0) continue;
+        const int count = bwd_unit(p, u, KV).count;
         // The unit's resident pair.  (The previous unit's last S was read out
         // before its last dK / dQ, which waited for every warp's dS of that
         // step; its accumulators are read out by each warp's epilogue before
@@ -583,8 +485,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
     for (int round = 0; ok && round * G < p.units; ++round) {
       const int u = bwd_unit_of(round, cta, G);
       if (u >= p.units) continue;
-      const BwdUnit w = bwd_unit<SINKS>(p, u, KV);
-      if (SINKS && w.count <= 0) continue;
+      const BwdUnit w = bwd_unit(p, u, KV);
       const long long vec0 = static_cast<long long>(w.bh) * p.N;
       const int my_row = w.blk * 128 + r;  // key row (dkdv) or query row (dq)
       float my_lse2 = INFINITY, my_dsum = 0.f;
@@ -594,8 +495,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
       }
       for (int it = 0; it < w.count; ++it) {
         const int gs = g + it;
-        const BwdStep st = bwd_step<SINKS, KV>(w, it);
-        const int other0 = st.blk * 128;  // first streamed row of this step
+        const int other0 = (w.first + it) * 128;  // first streamed row of this step
         // dkdv: the statistics of the streamed query block's columns, lane l
         // holding column cb + l (+inf lse masks query rows past N); read by
         // shuffles below
@@ -603,10 +503,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
         if (KV) {
           const int qi = other0 + cb + lane;
           if (qi < p.N) {
-            const long long at =
-                (SINKS ? (static_cast<long long>(w.b) * p.H + st.h) * p.N : vec0) + qi;
-            col_lse2 = p.lse[at] * kLog2e;
-            col_dsum = p.dsum[at];
+            col_lse2 = p.lse[vec0 + qi] * kLog2e;
+            col_dsum = p.dsum[vec0 + qi];
           }
         }
         ok = wait_phase(bars + 8 * C::B_SD_FULL, gs & 1, abort_flag, lim,
@@ -624,22 +522,6 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * C::B_S_READ);
-        // SINKS: this row's visible columns, [near_lo, near_hi] and for dQ those
-        // below sink_hi.  dkdv: row = key, columns = queries (for a sink key all
-        // from its own position on; columns past N carry lse = +inf); dq: row =
-        // query, columns = keys.
-        int near_lo = 0, near_hi = 127, sink_hi = 0;
-        if constexpr (SINKS) {
-          const int rel = my_row - other0;
-          if (KV) {
-            near_lo = rel;
-            if (p.window >= 0 && my_row >= p.sinks) near_hi = rel + p.window;
-          } else {
-            near_hi = rel;
-            if (p.window >= 0) near_lo = rel - p.window;
-            sink_hi = p.sinks - other0;
-          }
-        }
         // P (kept in fp32 over the S registers for dS); BWD_POLY8 of every 8
         // argument pairs take the FMA-pipe exp2, the rest ex2
         uint32_t pk[16];
@@ -663,12 +545,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
             const int c = cb + 2 * q + e;
             // dkdv: row = key my_row, column = query other0 + c (columns past N
             // carry lse = +inf); dq: row = query my_row, column = key other0 + c
-            bool vis;
-            if constexpr (SINKS)
-              vis = KV ? (c >= near_lo && c <= near_hi) : (c <= near_hi && (c >= near_lo || c < sink_hi));
-            else
-              vis = KV ? (!p.causal || other0 + c >= my_row)
-                       : (other0 + c < p.N && (!p.causal || other0 + c <= my_row));
+            const bool vis = KV ? (!p.causal || other0 + c >= my_row)
+                                : (other0 + c < p.N && (!p.causal || other0 + c <= my_row));
             pp[e] = vis ? pp[e] : 0.f;
             sd[2 * q + e] = __float_as_uint(pp[e]);
           }
@@ -718,9 +596,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
             uint32_t a0[32], a1[32];
             tmem_ld32_sync(lane_base + C::ACC0_COL + c, a0);
             if (KV) tmem_ld32_sync(lane_base + C::ACC1_COL + c, a1);
-            if (SINKS && KV && w.part >= 0) {
-              store_part<32>(p.parts, w.part, HD, r, c, a0, a1);
-            } else if (my_row < p.N) {
+            if (my_row < p.N) {
               if (KV) {
                 store_acc<BF16, 32>(static_cast<T*>(p.dv) + row_off + c, a0, 1.f, vec32);
                 store_acc<BF16, 32>(static_cast<T*>(p.dk) + row_off + c, a1, p.scale, vec32);
@@ -733,9 +609,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
             uint32_t a0[16], a1[16];
             tmem_ld16_sync(lane_base + C::ACC0_COL + c, a0);
             if (KV) tmem_ld16_sync(lane_base + C::ACC1_COL + c, a1);
-            if (SINKS && KV && w.part >= 0) {
-              store_part<16>(p.parts, w.part, HD, r, c, a0, a1);
-            } else if (my_row < p.N) {
+            if (my_row < p.N) {
               if (KV) {
                 store_acc<BF16, 16>(static_cast<T*>(p.dv) + row_off + c, a0, 1.f, vec32);
                 store_acc<BF16, 16>(static_cast<T*>(p.dk) + row_off + c, a1, p.scale, vec32);
@@ -758,40 +632,6 @@ __global__ void __launch_bounds__(BwdCfg<HD, KV>::THREADS, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-}
-
-// dV and dK of the sink blocks: the pieces' partial sums added in order, dK
-// times the scale, rounded once.  A thread takes 4 columns of one row.
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) sinks_sum_kernel(const __grid_constant__ BwdParams p) {
-  constexpr int C4 = HD / 4;
-  const int Hk = p.H / p.group;
-  const long long n = static_cast<long long>(p.B) * Hk * p.sink_blocks * 2 * 128 * C4;
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int c = static_cast<int>(i % C4) * 4;
-  const int r = static_cast<int>(i / C4 % 128);
-  const int which = static_cast<int>(i / (C4 * 128) % 2);  // 0: dV, 1: dK
-  const long long block = i / (C4 * 128 * 2);
-  const int blk = static_cast<int>(block % p.sink_blocks);
-  const long long bh = block / p.sink_blocks;
-  const int row = blk * 128 + r;
-  if (row >= p.N) return;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int piece = 0; piece < p.pieces; ++piece) {
-    int first, end;
-    sink_piece(p, blk, piece, &first, &end);
-    if (first >= end) break;
-    const float4 v = __ldg(reinterpret_cast<const float4*>(
-        p.parts + (((block * p.pieces + piece) * 2 + which) * 128 + r) * HD + c));
-    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-  }
-  const float mul = which ? p.scale : 1.f;
-  uint2 w = make_uint2(pack2<BF16>(t.x * mul, t.y * mul), pack2<BF16>(t.z * mul, t.w * mul));
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  T* out = static_cast<T*>(which ? p.dk : p.dv);
-  *reinterpret_cast<uint2*>(out + (bh * p.N + row) * HD + c) = w;
 }
 
 }  // namespace fa_sm100

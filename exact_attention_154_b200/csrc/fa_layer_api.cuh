@@ -6,6 +6,7 @@
 
 #include "fa_decode.cuh"
 #include "fa_rope.cuh"
+#include "fa_sinks_bwd_sm100.cuh"
 
 namespace {
 
@@ -204,15 +205,18 @@ int launch_fwd_sinks(const FwdParams& p, DeviceState& st, int dev, cudaStream_t 
 
 // How the dK/dV kernel splits a sink block's query blocks: into pieces about
 // as long as the other key blocks' share of a head (window + 2 blocks), at
-// most so many that the pieces of all sink blocks hold no more sums than the
-// head has key blocks.
-void sink_pieces(int N, int window, int sinks, int* sink_blocks, int* pieces, int* piece_blocks) {
+// most 32 steps over the group's heads (measured: 68-step pieces cost a long
+// sequence 7%, 16-step ones a short window 2%), and at most so many that the pieces
+// of all sink blocks hold no more sums than the head has key blocks.
+void sink_pieces(int N, int window, int sinks, int group, int* sink_blocks, int* pieces,
+                 int* piece_blocks) {
   const int nblk = (N + 127) / 128;
   *sink_blocks = window < 0 ? 0 : (sinks + 127) / 128;
   *pieces = 1;
   *piece_blocks = nblk;
   if (*sink_blocks == 0) return;
-  const int share = (window + 127) / 128 + 2;
+  int share = (window + 127) / 128 + 2;
+  if (share > (32 + group - 1) / group) share = (32 + group - 1) / group;
   int want = (nblk + share - 1) / share;
   if (want > nblk / *sink_blocks) want = nblk / *sink_blocks;
   if (want <= 1) return;
@@ -224,36 +228,59 @@ long long sink_part_floats(int B, int Hk, int d, int sink_blocks, int pieces) {
   return pieces > 1 ? (long long)B * Hk * sink_blocks * pieces * 2 * 128 * d : 0;
 }
 
+// The dK/dV kernel is persistent, a CTA an SM.  The dQ kernel may start beside
+// it (programmatic dependent launch), filling the SMs that the dK/dV kernel's
+// few long units leave one by one; so its CTAs are short, 16 steps or one unit.
 template <int HD, bool BF16, bool KV>
-int launch_bwd_sinks_kernel(const BwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
-  using C = BwdCfg<HD, KV>;
-  auto kernel = fa_bwd_kernel<HD, BF16, KV, true>;
+int launch_sinks_bwd_kernel(const SinksBwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
+  using C = SinksBwdCfg<HD, KV>;
+  auto kernel = sinks_bwd_kernel<HD, BF16, KV>;
   const int slot = (HD == 64 ? 0 : 4) + (BF16 ? 2 : 0) + (KV ? 1 : 0);
   const int rc = ensure_smem_attr(g_sinks[dev].bwd_attr[slot], kernel, C::SMEM_BYTES);
   if (rc != FA_OK) return rc;
-  const int grid = p.units < st.sm_count ? p.units : st.sm_count;
-  kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  int grid = p.units < st.sm_count ? p.units : st.sm_count;
+  if (!KV) {
+    const int steps = p.window < 0 ? p.nblk : (p.window + 127) / 128 + 1 + p.sink_blocks;
+    const int each = steps < p.nblk && steps < 16 ? 16 / steps : 1;
+    grid = (p.units + each - 1) / each;
+  }
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = KV ? 0 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
 }
 
 template <int HD, bool BF16>
-int launch_bwd_sinks(BwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
-  const int Hk = p.H / p.group;
+int launch_sinks_bwd(SinksBwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
   const long long rows = (long long)p.B * p.H * p.N;
   constexpr long long kRowsPerBlock = 256 / (HD / 8);  // bwd_dsum_kernel: HD / 8 threads a row
   bwd_dsum_kernel<HD, BF16><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0,
                               stream>>>(p.o, p.dout, p.dsum, rows);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  p.units = p.B * Hk * (p.sink_blocks * p.pieces + p.nblk - p.sink_blocks);
-  int rc = launch_bwd_sinks_kernel<HD, BF16, true>(p, st, dev, stream);
+  p.units = p.B * p.Hk * (p.sink_blocks * p.pieces + p.nblk - p.sink_blocks);
+  int rc = launch_sinks_bwd_kernel<HD, BF16, true>(p, st, dev, stream);
   if (rc != FA_OK) return rc;
+  p.units = p.B * p.H * p.nblk;
+  if ((rc = launch_sinks_bwd_kernel<HD, BF16, false>(p, st, dev, stream)) != FA_OK) return rc;
   if (p.pieces > 1) {
-    const long long n = (long long)p.B * Hk * p.sink_blocks * 2 * 128 * (HD / 4);
+    const long long n = (long long)p.B * p.Hk * p.sink_blocks * 2 * 128 * (HD / 4);
     sinks_sum_kernel<HD, BF16><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
-  p.units = p.B * p.H * p.nblk;
-  return launch_bwd_sinks_kernel<HD, BF16, false>(p, st, dev, stream);
+  return FA_OK;
 }
 
 // ------------------------------------------------------ one token at a time
@@ -421,7 +448,7 @@ long long fa_bwd_sinks_workspace(int B, int H, int Hk, int N, int d, int window,
   if (rc == FA_OK && d > 128) rc = FA_ERR_HEADDIM;
   if (rc != FA_OK) return rc;
   int sink_blocks, pieces, piece_blocks;
-  sink_pieces(N, window, sinks, &sink_blocks, &pieces, &piece_blocks);
+  sink_pieces(N, window, sinks, H / Hk, &sink_blocks, &pieces, &piece_blocks);
   return sink_part_floats(B, Hk, d, sink_blocks, pieces) + (long long)B * H * N;
 }
 
@@ -439,10 +466,10 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
     if (!aligned16(t)) return FA_ERR_ALIGN;
   if (!aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0) return FA_ERR_ALIGN;
   if ((rc = check_strides(q_strides, k_strides, v_strides, B, H, Hk, N, d)) != FA_OK) return rc;
-  BwdParams p;
+  SinksBwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.nblk = (N + 127) / 128;
-  sink_pieces(N, window, sinks, &p.sink_blocks, &p.pieces, &p.piece_blocks);
+  sink_pieces(N, window, sinks, H / Hk, &p.sink_blocks, &p.pieces, &p.piece_blocks);
   if ((long long)B * H * p.nblk > 0x7fffffffLL ||
       (long long)B * Hk * (p.sink_blocks * (long long)p.pieces + p.nblk) > 0x7fffffffLL)
     return FA_ERR_ARG;
@@ -463,17 +490,16 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
   p.dq = dq, p.dk = dk, p.dv = dv;
   p.out_vec32 = ((reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk) |
                   reinterpret_cast<uintptr_t>(dv)) & 31u) == 0;
-  p.B = B, p.H = H, p.N = N;
-  p.causal = 1;
-  p.window = window, p.sinks = sinks, p.group = H / Hk;
+  p.B = B, p.H = H, p.Hk = Hk, p.group = H / Hk, p.N = N;
+  p.window = window, p.sinks = sinks;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == FA_BF16;
   if (d == 64)
-    return bf16 ? launch_bwd_sinks<64, true>(p, *st, dev, s) : launch_bwd_sinks<64, false>(p, *st, dev, s);
-  return bf16 ? launch_bwd_sinks<128, true>(p, *st, dev, s) : launch_bwd_sinks<128, false>(p, *st, dev, s);
+    return bf16 ? launch_sinks_bwd<64, true>(p, *st, dev, s) : launch_sinks_bwd<64, false>(p, *st, dev, s);
+  return bf16 ? launch_sinks_bwd<128, true>(p, *st, dev, s) : launch_sinks_bwd<128, false>(p, *st, dev, s);
 }
 
 int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
