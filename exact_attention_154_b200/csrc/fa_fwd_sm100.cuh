@@ -91,6 +91,22 @@ enum Role : unsigned {
   kRoleStore = 6
 };
 
+// Division of a 31-bit number by a constant of the launch as a multiplication
+// (the round-up method of Granlund and Montgomery).
+struct FastDiv {
+  uint32_t mul, shift;
+  __host__ static FastDiv make(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    const uint64_t m = ((1ull << 32) * ((1ull << l) - d)) / d + 1;
+    return {static_cast<uint32_t>(m), l};
+  }
+  __device__ __forceinline__ int div(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n), t = __umulhi(mul, u);
+    return static_cast<int>((t + ((u - t) >> (shift > 0))) >> (shift > 0 ? shift - 1 : 0));
+  }
+};
+
 struct FwdParams {
   // 4-D (d, rows, H, batches) views of q, k, v; box 64 elements x 128 rows.
   // Fixed-length problems: rows = N, batches = B.  Variable-length problems
@@ -121,6 +137,7 @@ struct FwdParams {
   // Kernels with SINKS only: key j < sinks is visible from every query i >= j
   // whatever the window; query head h reads key / value head h / group.
   int sinks, group;
+  FastDiv div_bh, div_h, div_group;  // by B * H, H, group
 };
 
 // Bounded wait on an mbarrier phase.  Gives up when the CTA-wide abort flag
@@ -288,7 +305,7 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     // the one before, ...; with the snake hand-out below this balances the
     // triangular work to within a few percent
     const int nbh = p.B * p.H;
-    const int qi = t / nbh;
+    const int qi = SINKS ? p.div_bh.div(t) : t / nbh;
     bh = t - qi * nbh;
     qblock = p.num_qblocks - 1 - qi;
   } else {
@@ -296,7 +313,7 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     bh = t / p.num_qblocks;
     qblock = t - bh * p.num_qblocks;
   }
-  ti.b = bh / p.H;
+  ti.b = SINKS ? p.div_h.div(bh) : bh / p.H;
   ti.h = bh - ti.b * p.H;
   ti.q0 = qblock * BM * QS;
   if (p.cu_seqlens != nullptr) {
@@ -322,7 +339,7 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
   ti.lo_u = ti.lo[0];
   ti.n_u = ti.hi[0] == 0 ? 0 : max(ti.hi[0], ti.hi[1]) - ti.lo[0];
   if constexpr (SINKS) {
-    ti.hk = ti.h / p.group;
+    ti.hk = p.div_group.div(ti.h);
     ti.ns = p.window_left < 0 ? 0 : (p.sinks + BN - 1) / BN;
     ti.gap_end = max(ti.ns, ti.lo[0]);
     if (ti.hi[0] != 0) ti.n_u = max(ti.hi[0], ti.hi[1]) - (ti.gap_end - ti.ns);
@@ -476,7 +493,7 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
     }
 #pragma unroll 1
     for (int s = 0; ok && s < QS; ++s)
-      if (o_via_slot<C::O_TMA>(p, ti, s)) ok = reserve_slot();
+      if (o_via_slot<C::O_TMA && !SINKS>(p, ti, s)) ok = reserve_slot();
   }
   if (!ok) {
     // Let the loads already issued land before the CTA's shared memory goes away.
@@ -575,7 +592,7 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       tc_commit(bars + 8 * (C::B_KV_EMPTY + k_idx % KVS));
       if (jj + 1 == ti.n_u) tc_commit(bars + 8 * C::B_Q_EMPTY);
     }
-    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
+    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
   }
   if (!ok) {
     // Wait for every MMA this thread issued before TMEM is released.
@@ -662,7 +679,7 @@ __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       if (!ok) break;
       tc_commit(bars + 8 * (C::B_KV_EMPTY + v_idx % KVS));
     }
-    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
+    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
   }
   if (!ok) {
     volatile int no_abort = 0;
@@ -771,6 +788,11 @@ __device__ __forceinline__ void store_p_half_e4m3(uint32_t p_base, int r, int hf
                  pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
 }
 
+// The low n of 32 bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
 // ALIBI: the scaled score of key j gets -slope[h] * |i - j| (in the log2
 // domain, -slope[h] * log2(e) * |i - j|) before the row max is taken.
 template <int HD, int QS, int KVS, int ELT, bool ALIBI, bool SINKS>
@@ -824,11 +846,11 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
     // group follows the reservations of both tiles
     int o_slot = -1;
     uint32_t o_wait_par = 0u;
-    if (ti.n_u > 0) {
+    if (C::O_TMA && !SINKS && ti.n_u > 0) {
       int k = 0;
 #pragma unroll 1
       for (int s2 = 0; s2 < QS; ++s2) {
-        if (!o_via_slot<C::O_TMA>(p, ti, s2)) continue;
+        if (!o_via_slot<C::O_TMA && !SINKS>(p, ti, s2)) continue;
         const int slot = (kv_count + 2 * ti.n_u + k++) % KVS;
         if (s2 == s) {
           o_slot = slot;
@@ -870,12 +892,30 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
            (!SINKS || j * BN + BN > p.sinks)) ||
           (p.window_right >= 0 && j * BN + BN - 1 > r_first + p.window_right);
       const int kbase = j * BN + 64 * hf;  // key of this thread's first column
-      if (need_mask) {
+      bool none[2] = {false, false};
+      if (SINKS && need_mask) {
+        // The row's visible keys among each 32 of its 64 columns, as bits (keys
+        // past the sequence's end lie past every row's own position).  Most
+        // warps see all of 32 columns or none: the bits are only applied where
+        // they differ, and exponentials of none are not taken.
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rel = row - kbase - 32 * c;
+          uint32_t bits = low_bits(rel + 1);
+          if (p.window_left >= 0)
+            bits &= ~low_bits(rel - p.window_left) | low_bits(p.sinks - row + rel);
+          none[c] = __all_sync(0xffffffffu, bits == 0u);
+          if (!__all_sync(0xffffffffu, bits == ~0u)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              sv[32 * c + i] = (bits >> i) & 1u ? sv[32 * c + i] : -INFINITY;
+          }
+        }
+      } else if (need_mask) {
         const int lo_c = vis_lo - kbase, hi_c = vis_hi - kbase;
-        const int sink_c = SINKS ? p.sinks - kbase : 0;
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-          sv[c] = ((c >= lo_c || (SINKS && c < sink_c)) && c < hi_c) ? sv[c] : -INFINITY;
+          sv[c] = (c >= lo_c && c < hi_c) ? sv[c] : -INFINITY;
       }
       float m_half;
       if constexpr (ALIBI) {
@@ -918,7 +958,10 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       uint32_t pk[PK_WORDS];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (need_mask)
+        if (SINKS && none[c]) {
+#pragma unroll
+          for (int i = 0; i < PK_WORDS / 2; ++i) pk[(PK_WORDS / 2) * c + i] = 0u;
+        } else if (need_mask)
           softmax_chunk<ELT, 0>(sv + 32 * c, sl2e, neg_ref, pk + (PK_WORDS / 2) * c, acc);
         else
           softmax_chunk<ELT, poly_pairs_per8<HD>()>(sv + 32 * c, sl2e, neg_ref,
@@ -1070,11 +1113,11 @@ __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abor
     const TileInfo ti = decode_tile<QS, SINKS>(p, t);
     if (ti.n_u == 0) continue;
     const int kv0 = kv_count;
-    kv_count += 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
+    kv_count += 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
     int k = 0;
 #pragma unroll 1
     for (int s = 0; s < QS; ++s) {
-      if (!o_via_slot<C::O_TMA>(p, ti, s)) continue;
+      if (!o_via_slot<C::O_TMA && !SINKS>(p, ti, s)) continue;
       const int slot = (kv0 + 2 * ti.n_u + k++) % KVS;
       ok = wait_phase(bars + 8 * (C::B_O_STAGED + slot), (staged_par >> slot) & 1u, abort_flag,
                       p.wait_limit_ns, (kRoleStore << 8) | kSiteOStaged);
@@ -1144,7 +1187,7 @@ __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
     tma_prefetch_desc(&p.tmap_q);
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
-    if (C::O_TMA) tma_prefetch_desc(&p.tmap_o);
+    if (C::O_TMA && !SINKS) tma_prefetch_desc(&p.tmap_o);
   }
   if (warp == C::MMA_S_WARP) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
@@ -1171,7 +1214,7 @@ __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
   } else if (warp == C::MMA_PV_WARP) {
     if (lane == 0) mma_pv_role<HD, QS, KVS, ELT, SINKS>(p, base, tmem, abort_flag);
   } else if (warp == C::STORE_WARP) {
-    if (lane == 0 && C::O_TMA) store_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
+    if (lane == 0 && C::O_TMA && !SINKS) store_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
   }
 
   tc_fence_before_sync();

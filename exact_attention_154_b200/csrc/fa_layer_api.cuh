@@ -426,6 +426,9 @@ int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* ls
   p.window_right = 0;
   p.sinks = sinks;
   p.group = H / Hk;
+  p.div_bh = FastDiv::make((uint32_t)B * H);
+  p.div_h = FastDiv::make(H);
+  p.div_group = FastDiv::make(p.group);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o_scale = 1.f;
   p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;

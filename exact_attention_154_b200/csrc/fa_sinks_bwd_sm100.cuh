@@ -121,11 +121,6 @@ struct SinksBwdCfg {
   }
 };
 
-// The low n of 32 bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
-}
-
 // One unit of work.
 struct SinksUnit {
   int bh, blk, b, h;  // dK/dV: (b, key head h) and key block; dQ: (b, query head h), query block

@@ -354,7 +354,7 @@ def _check_rows(t: torch.Tensor, name: str, dtype=None):
     """A 16-bit CUDA tensor [B, H, N, d] whose rows are adjacent elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DT or (dtype is not None and t.dtype != dtype):
+    if t.dtype is not dtype and (t.dtype not in _DT or dtype is not None):
         raise ValueError(f"{name} must be float16 or bfloat16, one type for all operands")
     if t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be [B, H, N, d] with adjacent elements in a row")
@@ -370,19 +370,20 @@ def _strides(t: torch.Tensor):
     return None if t.is_contiguous() else _stride_array(*t.stride()[:3])
 
 
-def _launch(what: str, dev: torch.device, named, args):
-    """Calls entry point ``what`` with ``args`` and the current stream of ``dev``,
-    with that device current; ``named`` are the call's tensors (or None), which
-    must all live on it.  Raises what the library refuses."""
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    fn = getattr(load(), what)
-    if torch._C._cuda_getDevice() == dev.index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+def _launch(what: str, names: str, tensors, args):
+    """Calls entry point ``what`` with ``args`` and the current stream of the first
+    of ``tensors``, with its device current.  The others (or None; ``names`` are
+    theirs) must live on that device.  Raises what the library refuses."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            same_device((n, x) for n, x in zip(names.split(), tensors) if x is not None)
+    fn = getattr(_lib or load(), what)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with _on(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with _on(tensors[0].device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != FA_OK:
         raise FaError(rc, what)
 
@@ -411,30 +412,34 @@ def _fresh_rows(t: torch.Tensor):
     return True
 
 
+def _fits(t, dtype, shape) -> bool:
+    """Whether ``t`` is a contiguous tensor of this type and shape."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
+        and t.is_contiguous()
+
+
 def _table(cos, sin, positions, B, N):
     """Checks of the cos / sin table and the positions; (max_pos, rot)."""
-    for name, t in (("cos", cos), ("sin", sin)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 2 \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 [max_pos, rot / 2] tensor")
-    if cos.shape != sin.shape:
-        raise ValueError("cos and sin must share one shape")
-    if positions is not None and (not isinstance(positions, torch.Tensor)
-                                  or positions.dtype != torch.int32
-                                  or positions.shape != (B, N) or not positions.is_contiguous()):
+    shape = cos.shape if isinstance(cos, torch.Tensor) else ()
+    if len(shape) != 2 or not _fits(cos, torch.float32, shape) \
+            or not _fits(sin, torch.float32, shape):
+        raise ValueError("cos and sin must be contiguous float32 [max_pos, rot / 2] tensors")
+    if positions is not None and not _fits(positions, torch.int32, (B, N)):
         raise ValueError("positions must be a contiguous int32 [B, N] tensor")
-    return cos.shape[0], 2 * cos.shape[1]
+    return shape[0], 2 * shape[1]
 
 
 def _weights(q_weight, k_weight, d, dtype):
     """Checks of the norm weights; the type code the library is told."""
-    given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
-    for name, w in given:
-        if not isinstance(w, torch.Tensor) or w.shape != (d,) or not w.is_contiguous() \
-                or w.dtype not in (dtype, torch.float32) or w.dtype != given[0][1].dtype:
-            raise ValueError(f"{name} must be a contiguous [d] tensor of the operands' type or "
-                             "float32, both weights of one type")
-    return FA_FP32 if given and given[0][1].dtype == torch.float32 else _DT[dtype]
+    first = k_weight if q_weight is None else q_weight
+    if first is None:
+        return _DT[dtype]
+    wt = first.dtype if isinstance(first, torch.Tensor) else None
+    if wt not in (dtype, torch.float32) or not _fits(first, wt, (d,)) \
+            or (k_weight is not None and k_weight is not first and not _fits(k_weight, wt, (d,))):
+        raise ValueError("q_weight and k_weight must be contiguous [d] tensors of the operands' "
+                         "type or float32, both of one type")
+    return FA_FP32 if wt is torch.float32 else _DT[dtype]
 
 
 def _ptr(t):
@@ -483,7 +488,7 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
         lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
     else:
         _check_lse(lse, (B, H, N))
-    _launch("fa_fwd_sinks", q.device, (("k", k), ("v", v), ("out", out), ("lse", lse)),
+    _launch("fa_fwd_sinks", "q k v out lse", (q, k, v, out, lse),
             (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _strides(q),
              _strides(k), _strides(v), B, H, Hk, N, d, int(window), int(sinks),
              0.0 if scale is None else float(scale), _DT[q.dtype]))
@@ -508,8 +513,7 @@ def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor
         raise FaError(int(floats), "fa_bwd_sinks_workspace")
     dq, dk, dv = _new_like(q), _new_like(k), _new_like(v)
     ws = lse.new_empty((floats,))
-    _launch("fa_bwd_sinks", q.device,
-            (("k", k), ("v", v), ("o", o), ("lse", lse), ("dout", dout)),
+    _launch("fa_bwd_sinks", "q k v o lse dout", (q, k, v, o, lse, dout),
             (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _strides(q),
              _strides(k), _strides(v), ws.data_ptr(), B, H, Hk, N, d, int(window), int(sinks),
@@ -544,8 +548,8 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
         _check_tensor(out, "out")
         if out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must match q")
-    lse = torch.empty((B, H), device=q.device, dtype=torch.float32) if return_lse else None
-    _launch("fa_decode_sinks", q.device, (("k", k), ("v", v), ("seqlens", seqlens), ("out", out)),
+    lse = q.new_empty((B, H), dtype=torch.float32) if return_lse else None
+    _launch("fa_decode_sinks", "q k v seqlens out", (q, k, v, seqlens, out),
             (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
              seqlens.data_ptr(), _strides(k), _strides(v), B, H, Hk, S, d, int(window), int(sinks),
              0.0 if scale is None else float(scale), _DT[q.dtype]))
@@ -569,7 +573,7 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "no
         raise ValueError("max_pos and rot must be positive")
     cos = torch.empty((max_pos, rot // 2), device=dev, dtype=torch.float32)
     sin = torch.empty_like(cos)
-    _launch("fa_rope_table", cos.device, (),
+    _launch("fa_rope_table", "cos", (cos,),
             (cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base), ROPE_SCALING[scaling],
              float(factor), int(original_max_pos)))
     return cos, sin
@@ -597,19 +601,21 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch
         raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
     max_pos, rot = _table(cos, sin, positions, B, N)
     wt = _weights(q_weight, k_weight, d, q.dtype)
+    qo = ko = None  # strides of given outputs
     if q_out is None:
         q_out = _new_like(q)
     else:
         _check_out(q_out, "q_out", q)
+        qo = _strides(q_out)
     if k_out is None:
         k_out = _new_like(k)
     else:
         _check_out(k_out, "k_out", k)
-    _launch("fa_qk_norm_rope", q.device,
-            (("k", k), ("cos", cos), ("sin", sin), ("positions", positions),
-             ("q_weight", q_weight), ("k_weight", k_weight), ("q_out", q_out), ("k_out", k_out)),
+        ko = _strides(k_out)
+    _launch("fa_qk_norm_rope", "q k cos sin positions q_weight k_weight q_out k_out",
+            (q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out),
             (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _strides(q),
-             _strides(k), _strides(q_out), _strides(k_out), cos.data_ptr(), sin.data_ptr(),
+             _strides(k), qo, ko, cos.data_ptr(), sin.data_ptr(),
              _ptr(positions), max_pos, _ptr(q_weight), _ptr(k_weight), wt, float(eps), B, H, Hk, N,
              d, rot, int(bool(interleaved)), _DT[q.dtype]))
     return q_out, k_out
@@ -637,9 +643,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     ws = cos.new_empty((NORM_ROPE_PARTS, d))
-    _launch("fa_qk_norm_rope_bwd", q.device,
-            (("k", k), ("dq_out", dq_out), ("dk_out", dk_out), ("cos", cos), ("sin", sin),
-             ("positions", positions), ("q_weight", q_weight), ("k_weight", k_weight)),
+    _launch("fa_qk_norm_rope_bwd", "q k dq_out dk_out cos sin positions q_weight k_weight",
+            (q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight),
             (dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
              dk.data_ptr(), _ptr(dqw), _ptr(dkw), _strides(dq_out), _strides(dk_out), _strides(q),
              _strides(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions), max_pos, _ptr(q_weight),
