@@ -9,6 +9,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa_sm100.so")
+BINDING = os.path.join(PKG, "_fa_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
 SOURCES = ["fa_api.cu"]
 
 
@@ -44,7 +46,9 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library next to the package; returns its path."""
+    """Compile the library and its torch binding next to the package; returns
+    the library's path."""
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
@@ -58,6 +62,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
     check_register_split(res.stdout + res.stderr)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the torch side of the layer's calls (host code, resolved against
+    the library when it is loaded)."""
+    inputs = [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h")]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    include = [os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for p in include for x in ("-isystem", p)], "-o", tmp, BINDING_SOURCE,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-ldl"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 # The two-Q-tile kernels run 640 threads (96 registers each at launch) and

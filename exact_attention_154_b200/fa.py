@@ -1,14 +1,15 @@
 """Python binding of ``libfa_sm100.so`` (the C ABI in ``include/fa.h``).
 
 Argument marshalling only: torch supplies device memory and the current CUDA
-stream; every step of the attention forward runs in the library's kernel.
+stream; every step of the attention forward runs in the library's kernel.  The
+calls a model makes for every layer and token (norm and rotation, window and
+sinks) are marshalled by ``csrc/fa_torch.cpp``, the others through ctypes.
 There is no fallback: if the library is missing or the device is not an
 sm_100 GPU, the calls raise.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -20,13 +21,13 @@ from .synth import BF16, FP16
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa_sm100.so")
 _lock = threading.Lock()
 _lib = None
+_torch_calls = None
 
 FA_OK = 0
 FA_ERR_ARG, FA_ERR_ALIGN, FA_ERR_HEADDIM, FA_ERR_DTYPE = -1, -2, -3, -4
 FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_DEVICE = -5, -6, -7, -8
 FA_ERR_SEQLENS, FA_ERR_POSITIONS = -9, -10
 
-FA_FP32 = 3
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 NORM_ROPE_PARTS = 592
 
@@ -350,118 +351,27 @@ def bwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tens
     return dq, dk, dv
 
 
-def _check_rows(t: torch.Tensor, name: str, dtype=None):
-    """A 16-bit CUDA tensor [B, H, N, d] whose rows are adjacent elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype and (t.dtype not in _DT or dtype is not None):
-        raise ValueError(f"{name} must be float16 or bfloat16, one type for all operands")
-    if t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be [B, H, N, d] with adjacent elements in a row")
+def _calls():
+    """The compiled torch side of the calls below (``csrc/fa_torch.cpp``): their
+    argument checks, result tensors, device and stream."""
+    global _torch_calls
+    if _torch_calls is None:
+        load()
+        try:
+            from . import _fa_torch
+        except ImportError as e:
+            raise RuntimeError("the torch binding is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _fa_torch.load(_LIB_PATH)
+        _torch_calls = _fa_torch
+    return _torch_calls
 
 
-@functools.lru_cache(maxsize=256)
-def _stride_array(b, h, n):
-    return (ctypes.c_longlong * 3)(b, h, n)
-
-
-def _strides(t: torch.Tensor):
-    """The (batch, head, row) strides argument of the C ABI; None when contiguous."""
-    return None if t.is_contiguous() else _stride_array(*t.stride()[:3])
-
-
-def _launch(what: str, names: str, tensors, args):
-    """Calls entry point ``what`` with ``args`` and the current stream of the first
-    of ``tensors``, with its device current.  The others (or None; ``names`` are
-    theirs) must live on that device.  Raises what the library refuses."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            same_device((n, x) for n, x in zip(names.split(), tensors) if x is not None)
-    fn = getattr(_lib or load(), what)
-    if torch._C._cuda_getDevice() == index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with _on(tensors[0].device):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if rc != FA_OK:
-        raise FaError(rc, what)
-
-
-def _new_like(t: torch.Tensor):
-    """A new contiguous tensor of ``t``'s shape, type and device."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-def _check_out(t: torch.Tensor, name: str, like: torch.Tensor):
-    """A given output: its input's shape and type, rows that do not overlap."""
-    _check_rows(t, name, like.dtype)
-    if t.shape != like.shape or not _fresh_rows(t):
-        raise ValueError(f"{name} must have its input's shape and rows that do not overlap")
-
-
-def _fresh_rows(t: torch.Tensor):
-    """Whether the rows of [B, H, N, d] tensor ``t`` surely do not overlap: its
-    dimensions, ordered by stride, each step over the one before."""
-    need = 0
-    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
-                               key=lambda x: x[1]):
-        if stride <= need:
-            return False
-        need += (size - 1) * stride
-    return True
-
-
-def _fits(t, dtype, shape) -> bool:
-    """Whether ``t`` is a contiguous tensor of this type and shape."""
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
-        and t.is_contiguous()
-
-
-def _table(cos, sin, positions, B, N):
-    """Checks of the cos / sin table and the positions; (max_pos, rot)."""
-    shape = cos.shape if isinstance(cos, torch.Tensor) else ()
-    if len(shape) != 2 or not _fits(cos, torch.float32, shape) \
-            or not _fits(sin, torch.float32, shape):
-        raise ValueError("cos and sin must be contiguous float32 [max_pos, rot / 2] tensors")
-    if positions is not None and not _fits(positions, torch.int32, (B, N)):
-        raise ValueError("positions must be a contiguous int32 [B, N] tensor")
-    return shape[0], 2 * shape[1]
-
-
-def _weights(q_weight, k_weight, d, dtype):
-    """Checks of the norm weights; the type code the library is told."""
-    first = k_weight if q_weight is None else q_weight
-    if first is None:
-        return _DT[dtype]
-    wt = first.dtype if isinstance(first, torch.Tensor) else None
-    if wt not in (dtype, torch.float32) or not _fits(first, wt, (d,)) \
-            or (k_weight is not None and k_weight is not first and not _fits(k_weight, wt, (d,))):
-        raise ValueError("q_weight and k_weight must be contiguous [d] tensors of the operands' "
-                         "type or float32, both of one type")
-    return FA_FP32 if wt is torch.float32 else _DT[dtype]
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _check_qkv(q, k, v):
-    """Checks of [B, H, N, d] queries against [B, Hk, N, d] keys and values."""
-    _check_rows(q, "q")
-    _check_rows(k, "k", q.dtype)
-    _check_rows(v, "v", q.dtype)
-    B, H, N, d = q.shape
-    if k.shape != v.shape or k.shape != (B, k.shape[1], N, d) or k.shape[1] < 1 \
-            or H % k.shape[1] != 0:
-        raise ValueError("k and v must be [B, Hk, N, d] with q's B, N and d, H a multiple of Hk")
-    return B, H, k.shape[1], N, d
-
-
-def _check_lse(lse, shape):
-    if not isinstance(lse, torch.Tensor) or lse.shape != shape or lse.dtype != torch.float32 \
-            or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous {list(shape)} float32 tensor")
+def _done(what: str, result):
+    """The call's tensors; raises where the library returned a status instead."""
+    if result.__class__ is int:
+        raise FaError(result, what)
+    return result
 
 
 def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int,
@@ -475,24 +385,8 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
     shared by ``H / Hk`` query heads), of any strides with adjacent row elements.
     Returns ``(O [B, H, N, d], LSE [B, H, N])``, contiguous; LSE is None when
     ``return_lse`` is False."""
-    B, H, Hk, N, d = _check_qkv(q, k, v)
-    if out is None:
-        out = _new_like(q)
-    else:
-        _check_tensor(out, "out")
-        if out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must match q")
-    if not return_lse:
-        lse = None
-    elif lse is None:
-        lse = torch.empty((B, H, N), device=q.device, dtype=torch.float32)
-    else:
-        _check_lse(lse, (B, H, N))
-    _launch("fa_fwd_sinks", "q k v out lse", (q, k, v, out, lse),
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _strides(q),
-             _strides(k), _strides(v), B, H, Hk, N, d, int(window), int(sinks),
-             0.0 if scale is None else float(scale), _DT[q.dtype]))
-    return out, lse
+    return _done("fa_fwd_sinks", (_torch_calls or _calls()).fwd_sinks(
+        q, k, v, window, sinks, scale, out, lse, return_lse))
 
 
 def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
@@ -502,23 +396,8 @@ def bwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor
     ``(dq [B, H, N, d], dk, dv [B, Hk, N, d])``, contiguous; ``dk`` and ``dv``
     are summed over the query heads that share a key head.  ``o``, ``lse``: the
     forward's results; ``o`` and ``dout`` contiguous.  d is 64 or 128."""
-    B, H, Hk, N, d = _check_qkv(q, k, v)
-    for name, t in (("o", o), ("dout", dout)):
-        _check_tensor(t, name)
-        if t.shape != q.shape or t.dtype != q.dtype:
-            raise ValueError(f"{name} must match q")
-    _check_lse(lse, (B, H, N))
-    floats = load().fa_bwd_sinks_workspace(B, H, Hk, N, d, int(window), int(sinks))
-    if floats < 0:
-        raise FaError(int(floats), "fa_bwd_sinks_workspace")
-    dq, dk, dv = _new_like(q), _new_like(k), _new_like(v)
-    ws = lse.new_empty((floats,))
-    _launch("fa_bwd_sinks", "q k v o lse dout", (q, k, v, o, lse, dout),
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-             dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _strides(q),
-             _strides(k), _strides(v), ws.data_ptr(), B, H, Hk, N, d, int(window), int(sinks),
-             0.0 if scale is None else float(scale), _DT[q.dtype]))
-    return dq, dk, dv
+    return _done("fa_bwd_sinks", (_torch_calls or _calls()).bwd_sinks(
+        q, k, v, o, lse, dout, window, sinks, scale))
 
 
 def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: torch.Tensor,
@@ -530,30 +409,8 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
     ``seqlens[b]`` (int32 ``[B]``, the newest token included) are in use.
     Returns ``(O [B, H, d], LSE [B, H])``; a length of 0 gives O = 0 and LSE =
     -inf.  Cache rows that are not visible may hold anything."""
-    _check_tensor(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [B, H, d]")
-    B, H, d = q.shape
-    _check_rows(k, "k", q.dtype)
-    _check_rows(v, "v", q.dtype)
-    Hk, S = k.shape[1], k.shape[2]
-    if k.shape != v.shape or k.shape != (B, Hk, S, d) or Hk < 1 or H % Hk != 0:
-        raise ValueError("k and v must be [B, Hk, S, d] with q's B and d, H a multiple of Hk")
-    if not isinstance(seqlens, torch.Tensor) or seqlens.dtype != torch.int32 \
-            or seqlens.shape != (B,) or not seqlens.is_contiguous():
-        raise ValueError("seqlens must be a contiguous int32 [B] tensor")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_tensor(out, "out")
-        if out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must match q")
-    lse = q.new_empty((B, H), dtype=torch.float32) if return_lse else None
-    _launch("fa_decode_sinks", "q k v seqlens out", (q, k, v, seqlens, out),
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
-             seqlens.data_ptr(), _strides(k), _strides(v), B, H, Hk, S, d, int(window), int(sinks),
-             0.0 if scale is None else float(scale), _DT[q.dtype]))
-    return out, lse
+    return _done("fa_decode_sinks", (_torch_calls or _calls()).decode_sinks(
+        q, k, v, seqlens, window, sinks, scale, out, return_lse))
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "none",
@@ -573,9 +430,12 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "no
         raise ValueError("max_pos and rot must be positive")
     cos = torch.empty((max_pos, rot // 2), device=dev, dtype=torch.float32)
     sin = torch.empty_like(cos)
-    _launch("fa_rope_table", "cos", (cos,),
-            (cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base), ROPE_SCALING[scaling],
-             float(factor), int(original_max_pos)))
+    with _on(cos.device):
+        rc = load().fa_rope_table(cos.data_ptr(), sin.data_ptr(), max_pos, rot, float(base),
+                                  ROPE_SCALING[scaling], float(factor), int(original_max_pos),
+                                  _stream_ptr(cos))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rope_table")
     return cos, sin
 
 
@@ -593,32 +453,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch
     ``q_weight``, ``k_weight``: ``[d]``, or None to leave that operand
     unnormalised.  Returns ``(q_out, k_out)``, contiguous unless given; they
     may be ``q`` and ``k`` themselves."""
-    _check_rows(q, "q")
-    _check_rows(k, "k", q.dtype)
-    B, H, N, d = q.shape
-    Hk = k.shape[1]
-    if k.shape != (B, Hk, N, d):
-        raise ValueError("k must be [B, Hk, N, d] with q's B, N and d")
-    max_pos, rot = _table(cos, sin, positions, B, N)
-    wt = _weights(q_weight, k_weight, d, q.dtype)
-    qo = ko = None  # strides of given outputs
-    if q_out is None:
-        q_out = _new_like(q)
-    else:
-        _check_out(q_out, "q_out", q)
-        qo = _strides(q_out)
-    if k_out is None:
-        k_out = _new_like(k)
-    else:
-        _check_out(k_out, "k_out", k)
-        ko = _strides(k_out)
-    _launch("fa_qk_norm_rope", "q k cos sin positions q_weight k_weight q_out k_out",
-            (q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out),
-            (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _strides(q),
-             _strides(k), qo, ko, cos.data_ptr(), sin.data_ptr(),
-             _ptr(positions), max_pos, _ptr(q_weight), _ptr(k_weight), wt, float(eps), B, H, Hk, N,
-             d, rot, int(bool(interleaved)), _DT[q.dtype]))
-    return q_out, k_out
+    return _done("fa_qk_norm_rope", (_torch_calls or _calls()).qk_norm_rope(
+        q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out))
 
 
 def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -629,28 +465,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     its results; ``q``, ``k`` and the rest are the forward's arguments.
     Returns ``(dq, dk, dq_weight, dk_weight)``, the first two contiguous, the
     last two None where the weight is None."""
-    _check_rows(q, "q")
-    B, H, N, d = q.shape
-    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    for name, t, shape in (("k", k, (B, Hk, N, d)), ("dq_out", dq_out, q.shape),
-                           ("dk_out", dk_out, (B, Hk, N, d))):
-        _check_rows(t, name, q.dtype)
-        if t.shape != shape:
-            raise ValueError(f"{name} does not match q and k")
-    max_pos, rot = _table(cos, sin, positions, B, N)
-    wt = _weights(q_weight, k_weight, d, q.dtype)
-    dq, dk = _new_like(q), _new_like(k)
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = cos.new_empty((NORM_ROPE_PARTS, d))
-    _launch("fa_qk_norm_rope_bwd", "q k dq_out dk_out cos sin positions q_weight k_weight",
-            (q, k, dq_out, dk_out, cos, sin, positions, q_weight, k_weight),
-            (dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-             dk.data_ptr(), _ptr(dqw), _ptr(dkw), _strides(dq_out), _strides(dk_out), _strides(q),
-             _strides(k), cos.data_ptr(), sin.data_ptr(), _ptr(positions), max_pos, _ptr(q_weight),
-             _ptr(k_weight), wt, float(eps), ws.data_ptr(), B, H, Hk, N, d, rot,
-             int(bool(interleaved)), _DT[q.dtype]))
-    return dq, dk, dqw, dkw
+    return _done("fa_qk_norm_rope_bwd", (_torch_calls or _calls()).qk_norm_rope_bwd(
+        dq_out, dk_out, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved))
 
 
 def device_status(clear: bool = True):

@@ -126,6 +126,23 @@ def test_lengths_out_of_range_are_reported_and_skipped():
         check(q[b:b + 1], k[b:b + 1], v[b:b + 1], [lens[b]], 10, 1, out[b:b + 1], None)
 
 
+def test_refusals():
+    q, k, v = inputs(2, 4, 2, 30, 64, torch.bfloat16, 38)
+    lens = torch.tensor([3, 30], dtype=torch.int32).cuda()
+    for kw in (dict(q=q.float()), dict(q=q[:, :, None]), dict(q=q.transpose(0, 1)), dict(k=k.half()),
+               dict(k=k[:1]), dict(v=v[:, :, :9]), dict(seqlens=lens.long()), dict(seqlens=lens[:1]),
+               dict(seqlens=lens.cpu()), dict(out=q[:1]), dict(q=q[:, :3].contiguous())):
+        a = dict(q=q, k=k, v=v, seqlens=lens, window=8, sinks=2)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            fa.decode_sinks(**a)
+    for kw in (dict(window=-2), dict(sinks=-1), dict(scale=float("nan"))):
+        a = dict(q=q, k=k, v=v, seqlens=lens, window=8, sinks=2)
+        a.update(kw)
+        with pytest.raises(fa.FaError):
+            fa.decode_sinks(**a)
+
+
 def test_large_scores():
     q, k, v = inputs(2, 4, 2, 600, 128, torch.bfloat16, 34)
     q, k = q * 4, k * 4

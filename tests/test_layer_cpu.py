@@ -136,13 +136,6 @@ def test_python_norm_rope_refuses_cpu_and_bad_shapes():
         fa.rope_table(8, 64, device="cpu")
 
 
-def test_overlapping_rows_are_recognised():
-    x = torch.zeros(2, 3, 5, 64)
-    assert fa._fresh_rows(x) and fa._fresh_rows(x.transpose(1, 2)) and fa._fresh_rows(x[:, :, ::2])
-    assert not fa._fresh_rows(torch.zeros(1, 1, 5, 64).expand(2, 3, 5, 64))
-    assert not fa._fresh_rows(torch.zeros(1000).as_strided((1, 1, 5, 64), (1000, 1000, 32, 1)))
-
-
 # --------------------------------------------------- window and sinks
 
 def test_visible_by_its_words():

@@ -128,6 +128,39 @@ def test_in_place_and_strided_outputs():
     assert (cache[:, :, :20] == 5).all() and (cache[:, :, 70:] == 5).all()
 
 
+def test_refusals():
+    q, k = inputs(2, 3, 1, 5, 64, torch.bfloat16, 16)
+    cos, sin = fa.rope_table(8, 64)
+    w = weight(64, torch.bfloat16, 1)
+    flat = torch.zeros(1000, device="cuda", dtype=torch.bfloat16)
+    bad = [dict(q=q.float()), dict(k=k.half()), dict(k=k[:1]), dict(q=q[0]), dict(q=q[..., ::2]),
+           dict(cos=cos.double()), dict(cos=cos[:4]), dict(sin=sin.cpu()), dict(cos=cos[:, ::2], sin=sin[:, ::2]),
+           dict(positions=torch.zeros(2, 5, device="cuda", dtype=torch.int64)),
+           dict(positions=torch.zeros(2, 4, device="cuda", dtype=torch.int32)),
+           dict(q_weight=w[:32]), dict(q_weight=w.half()), dict(q_weight=w, k_weight=w.float()),
+           dict(q_weight=w.cpu()), dict(k_out=torch.empty_like(q)),
+           # rows of the output that overlap
+           dict(q_out=q[:1, :1].expand(2, 3, 5, 64)),
+           dict(k_out=flat.as_strided((2, 1, 5, 64), (320, 320, 32, 1))), dict(q_out=None, q=3)]
+    for kw in bad:
+        a = dict(q=q, k=k, cos=cos, sin=sin)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            fa.qk_norm_rope(**a)
+    for kw in (dict(cos=cos[:, :4].contiguous(), sin=sin[:, :4].contiguous()), dict(eps=-1.0),
+               dict(cos=cos[:3].contiguous(), sin=sin[:3].contiguous())):
+        a = dict(q=q, k=k, cos=cos, sin=sin)
+        a.update(kw)
+        with pytest.raises(fa.FaError):
+            fa.qk_norm_rope(**a)
+    with pytest.raises(ValueError):
+        fa.qk_norm_rope_bwd(q, q, q, k, cos, sin)
+    # strided outputs whose rows are apart are taken
+    out = torch.zeros(2, 5, 3, 64, device="cuda", dtype=torch.bfloat16).transpose(1, 2)
+    got = fa.qk_norm_rope(q, k, cos, sin, q_out=out)[0]
+    assert got.data_ptr() == out.data_ptr() and torch.equal(got, fa.qk_norm_rope(q, k, cos, sin)[0])
+
+
 def test_positions_outside_the_table_are_reported_and_skipped():
     q, k = inputs(1, 2, 1, 6, 64, torch.float16, 15)
     table = fa.rope_table(10, 64)

@@ -162,6 +162,33 @@ def test_outputs_given_and_no_lse():
     check_fwd(q, k, v, 30, 2, out, lse)
 
 
+def test_refusals():
+    q, k, v = qkv(2, 4, 2, 40, 64, torch.bfloat16, 535)
+    o, lse = fa.fwd_sinks(q, k, v, 8, 2)
+    for kw in (dict(q=q.float()), dict(k=k.half()), dict(k=k[:, :, :30]), dict(v=v[..., :32]), dict(v=v.cpu()),
+               dict(q=q[0]), dict(k=torch.cat((k, k[:, :1]), 1), v=torch.cat((v, v[:, :1]), 1)),
+               dict(out=o[:, :2]), dict(out=o.transpose(1, 2).contiguous().transpose(1, 2)),
+               dict(lse=lse.double()), dict(lse=lse[:, :, :5])):
+        a = dict(q=q, k=k, v=v, window=8, sinks=2)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            fa.fwd_sinks(**a)
+    for kw in (dict(window=-2), dict(sinks=-1), dict(scale=-1.0), dict(q=q[..., ::2].contiguous(),
+               k=k[..., ::2].contiguous(), v=v[..., ::2].contiguous())):
+        a = dict(q=q, k=k, v=v, window=8, sinks=2)
+        a.update(kw)
+        with pytest.raises(fa.FaError):
+            fa.fwd_sinks(**a)
+    for kw in (dict(o=o.half()), dict(lse=lse[:1]), dict(dout=o.transpose(1, 2)), dict(dout=o.cpu())):
+        a = dict(q=q, k=k, v=v, o=o, lse=lse, dout=o, window=8, sinks=2)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            fa.bwd_sinks(**a)
+    with pytest.raises(fa.FaError):
+        big = [torch.zeros(1, 2, 8, 256, device="cuda", dtype=torch.float16)] * 3
+        fa.bwd_sinks(*big, big[0], torch.zeros(1, 2, 8, device="cuda"), big[0], 4, 1)
+
+
 def test_large_scores():
     # logits of tens: the running reference moves, weights are nearly one-hot
     q, k, v = qkv(1, 2, 1, 600, 128, torch.bfloat16, 540)
