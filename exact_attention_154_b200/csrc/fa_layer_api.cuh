@@ -55,14 +55,15 @@ struct RopeArgs {
 
 template <int HD, bool BF16, bool INTER, bool BWD>
 int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
-  constexpr int kTokens = 32 / (HD / 8), kWarps = kRopeThreads / 32;
+  constexpr int kTokens = 32 / (HD / 16), kWarps = kRopeThreads / 32;
   const int HT = p.op[0].heads + p.op[1].heads;
   const long long groups = ((long long)p.B * p.N + kTokens - 1) / kTokens;
   p.blocks = (int)((groups + kWarps - 1) / kWarps);
   // heads a warp walks over: more of them share the loaded cos / sin, fewer
-  // give a small call more warps
+  // give a small call more warps (measured at 16384 tokens x 18 heads: 8 heads
+  // 32.4 us, 4: 32.7, 16: 37)
   int hpw = 1;
-  while (hpw < 16 && hpw < HT && groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
+  while (hpw < 8 && hpw < HT && groups * ((HT + 2 * hpw - 1) / (2 * hpw)) >= 32ll * st.sm_count)
     hpw *= 2;
   p.heads_per_warp = hpw;
   // CTAs in proportion to q's and k's items; the gradient's leave a row of
@@ -73,7 +74,8 @@ int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
     ctas[i] = (long long)p.blocks * p.chunks[i];
     if (ctas[i] > 1 << 30) return FA_ERR_ARG;
   }
-  const long long most = BWD ? FA_NORM_ROPE_PARTS : 1 << 20;
+  const long long wave = (long long)kRopeBwdCtas * st.sm_count;
+  const long long most = !BWD ? 1 << 20 : wave < FA_NORM_ROPE_PARTS ? wave : FA_NORM_ROPE_PARTS;
   if (ctas[0] + ctas[1] > most) {
     const long long k = most * p.op[1].heads / HT;
     ctas[1] = k < 1 ? 1 : k > most - 1 ? most - 1 : k;

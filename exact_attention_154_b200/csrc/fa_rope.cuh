@@ -15,13 +15,13 @@
 //
 // The statistics and both sums are fp32; each result is rounded once.
 //
-// What bounds it: memory.  Every row is read once and written once (the
-// gradient reads two), there is no reuse to tile for.  d / 8 lanes hold a row,
-// each two pieces of four columns chosen so that it holds whole pairs (columns
-// 4 l and rot/2 + 4 l on, or 8 l on when interleaved): no exchange between
-// lanes but the row's sum, and a warp's accesses still cover whole rows.  A
-// warp keeps its tokens' four cos / sin values in registers and walks over
-// heads of one operand, several rows in flight.
+// What bounds it: memory, if the instructions a row takes stay few.  Every row
+// is read once and written once (the gradient reads two), there is no reuse to
+// tile for.  d / 16 lanes hold a row, each two 16-byte pieces chosen so that it
+// holds whole pairs (columns 8 l and rot/2 + 8 l on, or 16 l on when
+// interleaved): no exchange between lanes but the row's sum.  A warp keeps its
+// tokens' eight cos / sin values a lane in registers and walks over heads of one
+// operand, the next row on its way.
 #pragma once
 
 #include "fa_fwd_sm100.cuh"
@@ -56,12 +56,12 @@ struct RopeParams {
   int blocks;     // blocks of a CTA's tokens (one token group a warp)
 };
 
-// Four 16-bit values as two pairs of fp32, and back.
+// Eight 16-bit values as four pairs of fp32, and back.
 template <bool BF16>
-__device__ __forceinline__ void unpack4(const uint2& v, float2* f) {
-  const uint32_t w[2] = {v.x, v.y};
+__device__ __forceinline__ void unpack8(const uint4& v, float2* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     if constexpr (BF16)
       f[i] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
     else
@@ -69,67 +69,78 @@ __device__ __forceinline__ void unpack4(const uint2& v, float2* f) {
   }
 }
 template <bool BF16>
-__device__ __forceinline__ uint2 pack4(const float2* f) {
-  return make_uint2(pack2<BF16>(f[0].x, f[0].y), pack2<BF16>(f[1].x, f[1].y));
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+  return make_uint4(pack2<BF16>(f[0].x, f[0].y), pack2<BF16>(f[1].x, f[1].y),
+                    pack2<BF16>(f[2].x, f[2].y), pack2<BF16>(f[3].x, f[3].y));
+}
+__device__ __forceinline__ void load_float8(const float* at, float2* f) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(at));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(at) + 1);
+  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 
-// Four consecutive weights as fp32, from the operands' type or from fp32.
+// Eight consecutive weights as fp32, from the operands' type or from fp32.
 template <bool BF16>
-__device__ __forceinline__ void load_weight4(const void* w, int w_fp32, int e, float2* f) {
+__device__ __forceinline__ void load_weight8(const void* w, int w_fp32, int e, float2* f) {
   if (w == nullptr) {
-    f[0] = f[1] = make_float2(1.f, 1.f);
+    f[0] = f[1] = f[2] = f[3] = make_float2(1.f, 1.f);
   } else if (w_fp32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + e));
-    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+    load_float8(static_cast<const float*>(w) + e, f);
   } else {
-    unpack4<BF16>(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + e)), f);
+    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + e)), f);
   }
 }
 
-// The other halves of the pairs that register pair k of a lane's eight columns
-// belongs to: the same places of the other piece, or its own two swapped.
+// The other halves of the pairs that register pair k of a lane's sixteen
+// columns belongs to: the same places of the other piece, or its own two swapped.
 template <bool INTER>
-__device__ __forceinline__ float2 partner(const float2 (&x)[4], int k) {
+__device__ __forceinline__ float2 partner(const float2 (&x)[8], int k) {
   if constexpr (INTER) return make_float2(x[k].y, x[k].x);
-  return x[k ^ 2];
+  return x[k ^ 4];
 }
 
 // Sum over the LANES lanes of a row.
 template <int LANES>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_dot(const float2 (&x)[8], const float2 (&y)[8]) {
+  float2 t = __fmul2_rn(x[0], y[0]), u = __fmul2_rn(x[1], y[1]);
+#pragma unroll
+  for (int k = 2; k < 8; k += 2) {
+    t = __ffma2_rn(x[k], y[k], t);
+    u = __ffma2_rn(x[k + 1], y[k + 1], u);
+  }
+  t = __fadd2_rn(t, u);
+  float v = t.x + t.y;
 #pragma unroll
   for (int sh = LANES / 2; sh > 0; sh >>= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
   return v;
 }
-template <int LANES>
-__device__ __forceinline__ float row_dot(const float2 (&x)[4], const float2 (&y)[4]) {
-  float2 t = __fmul2_rn(x[0], y[0]);
-#pragma unroll
-  for (int k = 1; k < 4; ++k) t = __ffma2_rn(x[k], y[k], t);
-  return row_sum<LANES>(t.x + t.y);
-}
 
-constexpr int kRopeThreads = 256;
+// Threads, and CTAs of an SM that the registers are limited for (80 and 128).
+// Measured on 16384 tokens x 18 heads of 128, forward / gradient: 32.4 / 53 us;
+// 64 registers (spilled) 41 / 83, 128 in the forward 37; d / 8 lanes a row with
+// 8-byte pieces 35 / 70 (its per-row instructions weigh twice as much), and the
+// same with rows through a ring of asynchronous copies 42 / 59.
+constexpr int kRopeThreads = 128;
+constexpr int kRopeFwdCtas = 6, kRopeBwdCtas = 4;
 
-// A CTA's item: up to heads_per_warp heads of q or k x one group of 32 / (HD / 8)
+// A CTA's item: up to heads_per_warp heads of q or k x one group of 32 / (HD / 16)
 // tokens for each warp.  Lanes without a token compute its last one again and
-// write nothing.
-// BWD: turns the arriving gradient back and takes it through the norm; each
-// CTA sums its rows' g * n and leaves the sums in `parts`.
+// write nothing.  BWD: turns the arriving gradient back and takes it through
+// the norm; each CTA sums its rows' g * n and leaves the sums in `parts`.
 template <int HD, bool BF16, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads, 4)
+__global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCtas)
     qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int LANES = HD / 8;         // lanes of a row
+  constexpr int LANES = HD / 16;        // lanes of a row
   constexpr int TOKENS = 32 / LANES;    // tokens of a warp item
   constexpr int WARPS = kRopeThreads / 32;
-  constexpr int U = BWD ? 1 : 2;        // rows in work; as many more are on their way
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int sub = lane % LANES;
   const int half = p.rot / 2;
-  // this lane's columns: ea .. ea + 3 and eb .. eb + 3
-  const bool turned = 8 * sub < p.rot;
-  const int ea = !INTER && turned ? 4 * sub : 8 * sub;
-  const int eb = !INTER && turned ? half + 4 * sub : 8 * sub + 4;
+  // this lane's columns: ea .. ea + 7 and eb .. eb + 7
+  const bool turned = 16 * sub < p.rot;
+  const int ea = !INTER && turned ? 8 * sub : 16 * sub;
+  const int eb = !INTER && turned ? half + 8 * sub : 16 * sub + 8;
   const bool is_k = static_cast<int>(blockIdx.x) >= p.ctas_q;
   const RopeOperand& op = p.op[is_k];
   const int cta = is_k ? blockIdx.x - p.ctas_q : blockIdx.x;
@@ -138,11 +149,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
   const bool normed = op.w != nullptr;
   const int tokens = p.B * p.N;
   const int items = p.blocks * chunks;
-  float2 w[4], dw[4];
-  load_weight4<BF16>(op.w, p.w_fp32, ea, w);
-  load_weight4<BF16>(op.w, p.w_fp32, eb, w + 2);
+  const long long xh = op.xh, gh = op.gh, yh = op.yh;
+  float2 w[8], dw[8];
+  if constexpr (BWD) {
+    load_weight8<BF16>(op.w, p.w_fp32, ea, w);
+    load_weight8<BF16>(op.w, p.w_fp32, eb, w + 4);
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) dw[k] = make_float2(0.f, 0.f);
+  for (int k = 0; k < 8; ++k) dw[k] = make_float2(0.f, 0.f);
 
 #pragma unroll 1
   for (int item = cta; item < items; item += ctas) {
@@ -153,28 +167,24 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     bool live = at_token < tokens;
     const int token = live ? static_cast<int>(at_token) : tokens - 1;
     const int b = token / p.N, n = token - b * p.N;
-    const uint16_t* x_at = static_cast<const uint16_t*>(op.x) + b * op.xb + h_begin * op.xh + n * op.xn;
-    const uint16_t* g_at = static_cast<const uint16_t*>(op.g) + b * op.gb + h_begin * op.gh + n * op.gn;
-    uint16_t* y_at = static_cast<uint16_t*>(op.y) + b * op.yb + h_begin * op.yh + n * op.yn;
-    // the rows of heads h .. h + U - 1 of the chunk
-    auto load = [&](int h, uint2 (&x)[U][2], uint2 (&g)[U][2]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h + u >= heads) break;
-        if (!BWD || normed) {
-          x[u][0] = *reinterpret_cast<const uint2*>(x_at + ea);
-          x[u][1] = *reinterpret_cast<const uint2*>(x_at + eb);
-          x_at += op.xh;
-        }
-        if constexpr (BWD) {
-          g[u][0] = *reinterpret_cast<const uint2*>(g_at + ea);
-          g[u][1] = *reinterpret_cast<const uint2*>(g_at + eb);
-          g_at += op.gh;
-        }
+    const uint16_t* x_at = static_cast<const uint16_t*>(op.x) + b * op.xb + h_begin * xh + n * op.xn;
+    const uint16_t* g_at = static_cast<const uint16_t*>(op.g) + b * op.gb + h_begin * gh + n * op.gn;
+    uint16_t* y_at = static_cast<uint16_t*>(op.y) + b * op.yb + h_begin * yh + n * op.yn;
+    // the row at x_at and g_at; moves on to the next head's
+    auto load = [&](uint4 (&x)[2], uint4 (&g)[2]) {
+      if (!BWD || normed) {
+        x[0] = *reinterpret_cast<const uint4*>(x_at + ea);
+        x[1] = *reinterpret_cast<const uint4*>(x_at + eb);
+        x_at += xh;
+      }
+      if constexpr (BWD) {
+        g[0] = *reinterpret_cast<const uint4*>(g_at + ea);
+        g[1] = *reinterpret_cast<const uint4*>(g_at + eb);
+        g_at += gh;
       }
     };
-    uint2 xv[U][2], gv[U][2];
-    load(0, xv, gv);  // before the position, which the cos / sin loads wait for
+    uint4 xv[2], gv[2];
+    load(xv, gv);  // before the position, which the cos / sin loads wait for
     int pos = n;
     if (p.positions != nullptr) pos = __ldg(p.positions + token);
     if (pos < 0 || pos >= p.max_pos) {
@@ -183,93 +193,97 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
       live = false;
       pos = 0;
     }
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 c[4], sn[4];  // of the lane's eight pairs
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = make_float2(1.f, 1.f), sn[k] = make_float2(0.f, 0.f);
     if (turned) {
-      const long long at = static_cast<long long>(pos) * half + 4 * sub;
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + at));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + at));
-      c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-      sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+      const long long at = static_cast<long long>(pos) * half + 8 * sub;
+      load_float8(p.cos + at, c);
+      load_float8(p.sin + at, sn);
     }
     // Forward: out = own * own_c + partner * other_c, the weights included
     // (first of a pair: a cos - b sin; second: b cos + a sin).  The gradient
     // turns back with c and sn as they are.
-    float2 own_c[4], other_c[4];
+    float2 own_c[8], other_c[8];
     if constexpr (!BWD) {
+      load_weight8<BF16>(op.w, p.w_fp32, ea, w);
+      load_weight8<BF16>(op.w, p.w_fp32, eb, w + 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         if constexpr (INTER) {
-          own_c[k] = make_float2(c[k], c[k]);
-          other_c[k] = make_float2(-sn[k], sn[k]);
+          const float ck = k & 1 ? c[k / 2].y : c[k / 2].x, sk = k & 1 ? sn[k / 2].y : sn[k / 2].x;
+          own_c[k] = make_float2(ck, ck);
+          other_c[k] = make_float2(-sk, sk);
         } else {
-          const float sg = k < 2 ? -1.f : 1.f;
-          own_c[k] = make_float2(c[2 * (k % 2)], c[2 * (k % 2) + 1]);
-          other_c[k] = make_float2(sg * sn[2 * (k % 2)], sg * sn[2 * (k % 2) + 1]);
+          const float sg = k < 4 ? -1.f : 1.f;
+          own_c[k] = c[k % 4];
+          other_c[k] = make_float2(sg * sn[k % 4].x, sg * sn[k % 4].y);
         }
         own_c[k] = __fmul2_rn(own_c[k], w[k]);
         other_c[k] = __fmul2_rn(other_c[k], partner<INTER>(w, k));
       }
     }
 #pragma unroll 1
-    for (int h0 = 0; h0 < heads; h0 += U) {
-      uint2 xn[U][2], gn[U][2];
-      load(h0 + U, xn, gn);
+    for (int h = 0; h < heads; ++h) {
+      float2 x[8], o[8];
+      if (!BWD || normed) {
+        unpack8<BF16>(xv[0], x);
+        unpack8<BF16>(xv[1], x + 4);
+      }
+      if constexpr (!BWD) {
+        if (h + 1 < heads) load(xv, gv);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h0 + u >= heads) break;
-        float2 x[4], y[4], o[4];
-        unpack4<BF16>(xv[u][0], x);
-        unpack4<BF16>(xv[u][1], x + 2);
-        if constexpr (BWD) {
-          unpack4<BF16>(gv[u][0], y);
-          unpack4<BF16>(gv[u][1], y + 2);
-        }
-        if constexpr (!BWD) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(partner<INTER>(x, k), other_c[k]));
-        } else if constexpr (INTER) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = make_float2(y[k].x * c[k] + y[k].y * sn[k], y[k].y * c[k] - y[k].x * sn[k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            o[k] = make_float2(y[k].x * c[2 * k] + y[k + 2].x * sn[2 * k],
-                               y[k].y * c[2 * k + 1] + y[k + 2].y * sn[2 * k + 1]);
-            o[k + 2] = make_float2(y[k + 2].x * c[2 * k] - y[k].x * sn[2 * k],
-                                   y[k + 2].y * c[2 * k + 1] - y[k].y * sn[2 * k + 1]);
-          }
-        }
+        for (int k = 0; k < 8; ++k)
+          o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(partner<INTER>(x, k), other_c[k]));
         if (normed) {
           const float r = rsqrtf(row_dot<LANES>(x, x) * (1.f / HD) + p.eps);
           const float2 rr = make_float2(r, r);
-          if constexpr (BWD) {
-            // o = g; n = x r; dn = g w; dx = r (dn - n mean(dn n))
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = __fmul2_rn(o[k], rr);
+        }
+      } else {
+        // o = g, the gradient turned back
+        {
+          float2 y[8];
+          unpack8<BF16>(gv[0], y);
+          unpack8<BF16>(gv[1], y + 4);
+          if (h + 1 < heads) load(xv, gv);
+          if constexpr (INTER) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float ck = k & 1 ? c[k / 2].y : c[k / 2].x, sk = k & 1 ? sn[k / 2].y : sn[k / 2].x;
+              o[k] = make_float2(y[k].x * ck + y[k].y * sk, y[k].y * ck - y[k].x * sk);
+            }
+          } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              x[k] = __fmul2_rn(x[k], rr);
-              if (live) dw[k] = __ffma2_rn(o[k], x[k], dw[k]);
-              o[k] = __fmul2_rn(o[k], w[k]);
+              o[k] = __ffma2_rn(y[k], c[k], __fmul2_rn(y[k + 4], sn[k]));
+              o[k + 4] = make_float2(y[k + 4].x * c[k].x - y[k].x * sn[k].x,
+                                     y[k + 4].y * c[k].y - y[k].y * sn[k].y);
             }
-            const float dot = row_dot<LANES>(o, x) * (-1.f / HD);
-            const float2 dd = make_float2(dot, dot);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = __ffma2_rn(x[k], dd, o[k]);
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = __fmul2_rn(o[k], rr);
         }
-        if (live) {
-          *reinterpret_cast<uint2*>(y_at + ea) = pack4<BF16>(o);
-          *reinterpret_cast<uint2*>(y_at + eb) = pack4<BF16>(o + 2);
-          y_at += op.yh;
+        if (normed) {
+          // n = x r; dn = g w; dx = r (dn - n mean(dn n))
+          const float r = rsqrtf(row_dot<LANES>(x, x) * (1.f / HD) + p.eps);
+          const float2 rr = make_float2(r, r);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            x[k] = __fmul2_rn(x[k], rr);
+            if (live) dw[k] = __ffma2_rn(o[k], x[k], dw[k]);
+            o[k] = __fmul2_rn(o[k], w[k]);
+          }
+          const float dot = row_dot<LANES>(o, x) * (-1.f / HD);
+          const float2 dd = make_float2(dot, dot);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = __fmul2_rn(__ffma2_rn(x[k], dd, o[k]), rr);
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) xv[u][i] = xn[u][i], gv[u][i] = gn[u][i];
+      if (live) {
+        *reinterpret_cast<uint4*>(y_at + ea) = pack8<BF16>(o);
+        *reinterpret_cast<uint4*>(y_at + eb) = pack8<BF16>(o + 4);
+      }
+      y_at += yh;
     }
   }
   if constexpr (BWD) {
@@ -277,11 +291,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     // the CTA's sums: lanes of different tokens, then the warps in order
     __shared__ float sums[WARPS][HD];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       float t = i & 1 ? dw[i / 2].y : dw[i / 2].x;
 #pragma unroll
       for (int sh = LANES; sh < 32; sh <<= 1) t += __shfl_xor_sync(0xffffffffu, t, sh);
-      if (lane < LANES) sums[warp][(i < 4 ? ea : eb - 4) + i] = t;
+      if (lane < LANES) sums[warp][(i < 8 ? ea : eb - 8) + i] = t;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < HD; i += kRopeThreads) {
