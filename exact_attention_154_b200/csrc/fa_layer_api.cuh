@@ -497,6 +497,9 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
                   reinterpret_cast<uintptr_t>(dv)) & 31u) == 0;
   p.B = B, p.H = H, p.Hk = Hk, p.group = H / Hk, p.N = N;
   p.window = window, p.sinks = sinks;
+  p.div_kv = FastDiv::make((uint32_t)B * Hk), p.div_q = FastDiv::make((uint32_t)B * H);
+  p.div_hk = FastDiv::make(Hk), p.div_h = FastDiv::make(H);
+  p.div_group = FastDiv::make(p.group), p.div_pieces = FastDiv::make(p.pieces);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();

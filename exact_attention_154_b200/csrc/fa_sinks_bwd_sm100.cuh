@@ -65,6 +65,7 @@ struct SinksBwdParams {
   int pieces, piece_blocks;  // of a sink block: pieces of that many query blocks
   float* parts;        // pieces > 1: fp32 [B, Hk, sink_blocks, pieces, {dV, dK}, 128, d]
   unsigned long long wait_limit_ns;
+  FastDiv div_kv, div_q, div_hk, div_h, div_group, div_pieces;  // by B Hk, B H, Hk, H, group, pieces
 };
 
 template <int HD, bool KV>
@@ -144,9 +145,9 @@ template <bool KV>
 __device__ __forceinline__ SinksUnit sinks_unit(const SinksBwdParams& p, int u) {
   SinksUnit w;
   const int nh = KV ? p.Hk : p.H, heads = p.B * nh;
-  const int rank = u / heads;
+  const int rank = (KV ? p.div_kv : p.div_q).div(u);
   w.bh = u - rank * heads;
-  w.b = w.bh / nh;
+  w.b = (KV ? p.div_hk : p.div_h).div(w.bh);
   w.h = w.bh - w.b * nh;
   w.part = -1;
   if (KV) {
@@ -155,7 +156,7 @@ __device__ __forceinline__ SinksUnit sinks_unit(const SinksBwdParams& p, int u) 
     int end;
     const int split = p.sink_blocks * p.pieces;
     if (rank < split) {
-      w.blk = rank / p.pieces;
+      w.blk = p.div_pieces.div(rank);
       const int piece = rank - w.blk * p.pieces;
       sink_piece(p, w.blk, piece, &w.first, &end);
       if (p.pieces > 1) w.part = (w.bh * p.sink_blocks + w.blk) * p.pieces + piece;
@@ -171,7 +172,7 @@ __device__ __forceinline__ SinksUnit sinks_unit(const SinksBwdParams& p, int u) 
     w.count = w.per_head * p.group;
   } else {
     w.blk = p.nblk - 1 - rank;
-    w.h0 = w.h / p.group;
+    w.h0 = p.div_group.div(w.h);
     const int lo = p.window < 0 ? 0 : max(0, w.blk * 128 - p.window) / 128;
     w.ns = min(p.sink_blocks, w.blk + 1);
     w.gap_end = max(w.ns, lo);
@@ -434,23 +435,24 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
       const SinksUnit w = sinks_unit<KV>(p, u);
       if (w.count <= 0) continue;
       const int my_row = w.blk * 128 + r;  // key row (dK/dV) or query row (dQ)
-      float my_nlse2 = -INFINITY, my_nd = 0.f;  // dQ: -(LSE log2 e), -D of the row
+      // Statistics are kept as loaded: scaling them here would wait for the load.
+      float my_lse = INFINITY, my_d = 0.f;  // dQ: LSE and D of the row
       if (!KV && my_row < p.N) {
         const long long at = static_cast<long long>(w.bh) * p.N + my_row;
-        my_nlse2 = -p.lse[at] * kLog2e;
-        my_nd = -p.dsum[at];
+        my_lse = __ldg(p.lse + at);
+        my_d = p.dsum[at];
       }
       SinksStep<KV> st(w);
       // dK/dV: the statistics of the streamed query block's columns, lane l
-      // holding column cb + l (-inf: a row past N, weight 0)
-      float col_nlse2 = -INFINITY, col_nd = 0.f;
+      // holding column cb + l (+inf: a row past N, weight 0)
+      float col_lse = INFINITY, col_d = 0.f;
       auto load_stats = [&]() {
         const int qi = st.blk * 128 + cb + lane;
-        col_nlse2 = -INFINITY, col_nd = 0.f;
+        col_lse = INFINITY, col_d = 0.f;
         if (qi < p.N) {
           const long long at = (static_cast<long long>(w.b) * p.H + st.h) * p.N + qi;
-          col_nlse2 = -p.lse[at] * kLog2e;
-          col_nd = -p.dsum[at];
+          col_lse = __ldg(p.lse + at);
+          col_d = p.dsum[at];
         }
       };
       if (KV) load_stats();
@@ -460,9 +462,12 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         // queries from the key's own position to the window's end (a sink
         // key's: to the end); dQ: the window's keys and the sinks.  Most warps
         // see all of their columns or none, so the bits are only applied where
-        // they differ.
-        uint32_t bits;
-        {
+        // they differ, and not even looked for in a block that is wholly visible
+        // (below the diagonal, inside the window).
+        uint32_t bits = ~0u;
+        bool all = true, none = false;
+        const int ahead = (KV ? st.blk - w.blk : w.blk - st.blk) * 128;  // of the query block
+        if (ahead < 128 || (p.window >= 0 && ahead + 127 > p.window)) {
           const int rel = my_row - st.blk * 128 - cb;
           if (KV) {
             bits = ~low_bits(rel);
@@ -471,8 +476,9 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
             bits = low_bits(rel + 1);
             if (p.window >= 0) bits &= ~low_bits(rel - p.window) | low_bits(p.sinks - st.blk * 128 - cb);
           }
+          all = __all_sync(0xffffffffu, bits == ~0u);
+          none = __all_sync(0xffffffffu, bits == 0u);
         }
-        const bool all = __all_sync(0xffffffffu, bits == ~0u), none = __all_sync(0xffffffffu, bits == 0u);
         ok = wait_phase(bars + 8 * C::B_S_FULL, gs & 1, abort_flag, lim,
                         (kRoleSoftmax << 8) | kSiteSFull);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -492,11 +498,12 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         const float4* stat = nullptr;
         if constexpr (KV) {
           float* to = reinterpret_cast<float*>(smem + C::STAT_OFF) + ((gs & 1) * 4 + grp) * 64;
-          to[lane] = col_nlse2;
-          to[32 + lane] = col_nd;
+          to[lane] = -col_lse * kLog2e;
+          to[32 + lane] = -col_d;
           stat = reinterpret_cast<const float4*>(to);
           __syncwarp();
         }
+        const float my_nlse2 = -my_lse * kLog2e;
         if (none) {
 #pragma unroll
           for (int q = 0; q < 16; ++q) pv[q] = make_float2(0.f, 0.f);
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         tmem_ld32_sync(lane_base + dpc + cb, sv);
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          float2 nd = make_float2(my_nd, my_nd);
+          float2 nd = make_float2(-my_d, -my_d);
           if constexpr (KV) {
             const float4 d4 = stat[8 + q / 2];
             nd = q % 2 ? make_float2(d4.z, d4.w) : make_float2(d4.x, d4.y);
