@@ -17,7 +17,7 @@ namespace {
 
 using namespace fa_sm100;
 
-constexpr int kVersion = 1 * 10000 + 2 * 100 + 0;  // 1.2.0: local window, ALiBi, varlen
+constexpr int kVersion = 1 * 10000 + 3 * 100 + 0;  // 1.3.0: window and sinks, norm and rotation
 // Limit of every mbarrier wait of the kernel (2 s unless the build sets it).
 #ifndef FA_WAIT_LIMIT_NS
 #define FA_WAIT_LIMIT_NS 2000000000ull
@@ -596,7 +596,7 @@ const char* fa_strerror(int status) {
     case FA_ERR_UNSUPPORTED: return "unsupported option (dropout_p must be 0)";
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "kernel gave up on a bounded wait";
-    case FA_ERR_SEQLENS: return "cu_seqlens out of range (seen by the kernel)";
+    case FA_ERR_SEQLENS: return "sequence offsets or cache lengths out of range (seen by the kernel)";
     case FA_ERR_POSITIONS: return "position outside the cos / sin table (seen by the kernel)";
     case FA_ERR_DEVICE: return "current device is not sm_100";
     default: return "unknown status";

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) decode_kernel(const __grid_
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const int rank = static_cast<int>(cluster_rank()), CL = static_cast<int>(cluster_size());
-  const int tile = blockIdx.y;
+  const int tile = blockIdx.x / CL;
   const int rt = tile % p.row_tiles;
   const int bh = tile / p.row_tiles;
   const int b = bh / p.Hk, hk = bh - b * p.Hk;

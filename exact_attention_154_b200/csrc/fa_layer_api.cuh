@@ -309,7 +309,7 @@ int launch_decode(DecodeParams& p, int B, DeviceState& st, int dev, cudaStream_t
   }
   p.row_tiles = (p.group + C::Q - 1) / C::Q;
   const long long tiles = (long long)B * p.Hk * p.row_tiles;
-  if (tiles > 65535) return FA_ERR_ARG;
+  if (tiles > 0x7fffffffLL / kDecodeMaxCluster) return FA_ERR_ARG;
   // Cluster size: two CTAs for every SM and no more (measured at 128 tiles of
   // 8192 keys: 2 CTAs a tile 78 us, 1: 84, 4: 86, 8: 85; at 32 tiles 8: 26 us,
   // 4: 28, 16: 44), and at least one step for every second warp (one tile pair
@@ -322,7 +322,7 @@ int launch_decode(DecodeParams& p, int B, DeviceState& st, int dev, cudaStream_t
     cl *= 2;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(cl, (unsigned)tiles);
+  cfg.gridDim = dim3((unsigned)(cl * tiles));
   cfg.blockDim = dim3(32 * kDecodeWarps);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;

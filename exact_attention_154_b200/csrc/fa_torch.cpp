@@ -130,6 +130,12 @@ int whole(PyObject* o) {
   return as_int(x);
 }
 
+int truth(PyObject* o) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) throw python_error();
+  return x;
+}
+
 // The result, or the library's status where it refused.
 PyObject* status(int rc) { return PyLong_FromLong(rc); }
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
@@ -236,7 +242,7 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
       static_cast<const float*>(data(*t.cos)), static_cast<const float*>(data(*t.sin)), t.positions,
       t.max_pos, w.ptr(0), w.ptr(1), w.code, static_cast<float>(number(a[7])), as_int(q.size(0)),
       as_int(q.size(1)), as_int(k.size(1)), as_int(q.size(2)), as_int(q.size(3)), t.rot,
-      PyObject_IsTrue(a[8]), dtype_code(q), on.get());
+      truth(a[8]), dtype_code(q), on.get());
   if (rc != FA_OK) return status(rc);
   PyObject* out[2] = {wrap(qo), wrap(ko)};
   return tuple(out);
@@ -265,7 +271,7 @@ PyObject* norm_rope_bwd(PyObject* const* a, Py_ssize_t n) {
       static_cast<const float*>(data(*t.cos)), static_cast<const float*>(data(*t.sin)), t.positions,
       t.max_pos, w.ptr(0), w.ptr(1), w.code, static_cast<float>(number(a[9])),
       static_cast<float*>(data(ws)), as_int(q.size(0)), as_int(q.size(1)), as_int(k.size(1)),
-      as_int(q.size(2)), as_int(q.size(3)), t.rot, PyObject_IsTrue(a[10]), dtype_code(q), on.get());
+      as_int(q.size(2)), as_int(q.size(3)), t.rot, truth(a[10]), dtype_code(q), on.get());
   if (rc != FA_OK) return status(rc);
   PyObject* out[4] = {wrap(dq), wrap(dk), w.w[0] ? wrap(dw[0]) : none(), w.w[1] ? wrap(dw[1]) : none()};
   return tuple(out);
@@ -290,7 +296,7 @@ PyObject* fwd_sinks(PyObject* const* a, Py_ssize_t n) {
   check_kv(k, v, q.size(0), q.size(1), q.size(2), q.size(3));
   const int window = whole(a[3]), sinks = whole(a[4]);
   const at::Tensor o = a[6] == Py_None ? new_like(q) : contiguous_like(a[6], "out", q);
-  const int with_lse = PyObject_IsTrue(a[8]);
+  const int with_lse = truth(a[8]);
   at::Tensor lse;
   if (with_lse)
     lse = a[7] == Py_None ? at::empty(q.sizes().slice(0, 3), q.options().dtype(at::kFloat))
@@ -350,7 +356,7 @@ PyObject* decode_sinks(PyObject* const* a, Py_ssize_t n) {
   same_device(lens, "seqlens", q);
   const int window = whole(a[4]), sinks = whole(a[5]);
   const at::Tensor o = a[7] == Py_None ? new_like(q) : contiguous_like(a[7], "out", q);
-  const int with_lse = PyObject_IsTrue(a[8]);
+  const int with_lse = truth(a[8]);
   at::Tensor lse;
   if (with_lse) lse = at::empty(q.sizes().slice(0, 2), q.options().dtype(at::kFloat));
   const OnDevice on(q);

@@ -304,8 +304,6 @@ int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, con
  *                and lse unwritten, and fa_device_status() returns FA_ERR_SEQLENS.
  *   window     : >= 0, or -1 (every cached key);  sinks : >= 0
  *   d          : 64, 128 or 256;  S <= 2^30;  scale as fa_fwd
- *   size       : at most 65535 tiles, B * Hk * ceil(H / Hk / 8), else FA_ERR_ARG (16
- *                in place of 8 where H / Hk > 8 and d < 256)
  *
  * A cache that keeps only the sinks and the newest keys (in any order) is
  * read with window = -1.  Deterministic; one launch, no scratch.

@@ -153,6 +153,19 @@ def test_large_scores():
     assert np.abs(layer.f64(lse) - L).max() <= 2.0 ** -9
 
 
+def test_more_tiles_than_a_grid_row_holds():
+    # 70,000 sequences x 1 key head: past 65535 tiles
+    B = 70000
+    g = torch.Generator(device="cuda").manual_seed(39)
+    q, k, v = (torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+               for s in ((B, 2, 64), (B, 1, 3, 64), (B, 1, 3, 64)))
+    lens = torch.randint(0, 4, (B,), generator=g, device="cuda").to(torch.int32)
+    o, lse = fa.decode_sinks(q, k, v, lens, 1, 1)
+    torch.cuda.synchronize()
+    at = [0, 1, 65534, 65535, 65536, B - 2, B - 1]
+    check(q[at], k[at], v[at], lens[at].tolist(), 1, 1, o[at], lse[at])
+
+
 def test_no_lse_and_repeatable():
     q, k, v = inputs(2, 8, 1, 5000, 128, torch.bfloat16, 35)
     a = run(q, k, v, [5000, 4321], -1, 0)
