@@ -91,22 +91,6 @@ enum Role : unsigned {
   kRoleStore = 6
 };
 
-// Division of a 31-bit number by a constant of the launch as a multiplication
-// (the round-up method of Granlund and Montgomery).
-struct FastDiv {
-  uint32_t mul, shift;
-  __host__ static FastDiv make(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    const uint64_t m = ((1ull << 32) * ((1ull << l) - d)) / d + 1;
-    return {static_cast<uint32_t>(m), l};
-  }
-  __device__ __forceinline__ int div(int n) const {
-    const uint32_t u = static_cast<uint32_t>(n), t = __umulhi(mul, u);
-    return static_cast<int>((t + ((u - t) >> (shift > 0))) >> (shift > 0 ? shift - 1 : 0));
-  }
-};
-
 struct FwdParams {
   // 4-D (d, rows, H, batches) views of q, k, v; box 64 elements x 128 rows.
   // Fixed-length problems: rows = N, batches = B.  Variable-length problems
@@ -134,10 +118,6 @@ struct FwdParams {
   int num_qblocks;   // query blocks per (b, h) (of the longest sequence)
   int num_tiles;     // B * H * num_qblocks
   unsigned long long wait_limit_ns;
-  // Kernels with SINKS only: key j < sinks is visible from every query i >= j
-  // whatever the window; query head h reads key / value head h / group.
-  int sinks, group;
-  FastDiv div_bh, div_h, div_group;  // by B * H, H, group
 };
 
 // Bounded wait on an mbarrier phase.  Gives up when the CTA-wide abort flag
@@ -243,12 +223,6 @@ struct FwdCfg {
 // needs the key blocks [lo[s], hi[s]) (empty: lo == hi == 0); the work tile
 // streams their union [lo_u, lo_u + n_u), which is contiguous because the Q
 // tiles are adjacent and every row sees its own key.
-//
-// With SINKS a tile also needs the blocks [0, ns) that hold the sinks (those
-// below hi[s]), and the work tile streams n_u blocks: [0, ns), then from
-// gap_end = max(ns, lo[0]) on.  Tile 0 uses every streamed block up to its
-// last (lo[0] <= lo[1] <= hi[0]), so a block's users are tile 0, tile 1 or
-// both, and after tile 0's last only tile 1.
 struct TileInfo {
   int b, h, q0;  // q0: first query row, relative to the sequence
   int len;       // the sequence's length (queries = keys)
@@ -256,29 +230,10 @@ struct TileInfo {
   int bc;        // tensor-map batch coordinate
   int lo[2], hi[2];
   int lo_u, n_u;
-  int hk;           // key / value head (SINKS; else h)
-  int ns, gap_end;  // SINKS
 };
 
-template <bool SINKS>
 __device__ __forceinline__ bool in_range(const TileInfo& ti, int s, int j) {
-  if constexpr (SINKS) return j < ti.hi[s] && (j < ti.ns || j >= ti.lo[s]);
   return j >= ti.lo[s] && j < ti.hi[s];
-}
-// The jj-th key block the work tile streams.
-template <bool SINKS>
-__device__ __forceinline__ int block_of(const TileInfo& ti, int jj) {
-  if constexpr (SINKS) return jj < ti.ns ? jj : jj - ti.ns + ti.gap_end;
-  return ti.lo_u + jj;
-}
-// The first key block of Q tile s, and the one after its block j.
-template <bool SINKS>
-__device__ __forceinline__ int first_block(const TileInfo& ti, int s) {
-  return SINKS && ti.ns > 0 ? 0 : ti.lo[s];
-}
-template <bool SINKS>
-__device__ __forceinline__ int block_after(const TileInfo& ti, int s, int j) {
-  return SINKS && j + 1 == ti.ns ? max(ti.ns, ti.lo[s]) : j + 1;
 }
 
 // Key blocks [lo, hi) a 128-row Q tile starting at row r0 of a sequence of
@@ -296,7 +251,7 @@ __device__ __forceinline__ void key_range(const FwdParams& p, int len, int r0, i
   hi = p.window_right < 0 ? nkv : min(len - 1, last_row + p.window_right) / BN + 1;
 }
 
-template <int QS, bool SINKS>
+template <int QS>
 __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
   TileInfo ti;
   int bh, qblock;
@@ -305,7 +260,7 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     // the one before, ...; with the snake hand-out below this balances the
     // triangular work to within a few percent
     const int nbh = p.B * p.H;
-    const int qi = SINKS ? p.div_bh.div(t) : t / nbh;
+    const int qi = t / nbh;
     bh = t - qi * nbh;
     qblock = p.num_qblocks - 1 - qi;
   } else {
@@ -313,7 +268,7 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     bh = t / p.num_qblocks;
     qblock = t - bh * p.num_qblocks;
   }
-  ti.b = SINKS ? p.div_h.div(bh) : bh / p.H;
+  ti.b = bh / p.H;
   ti.h = bh - ti.b * p.H;
   ti.q0 = qblock * BM * QS;
   if (p.cu_seqlens != nullptr) {
@@ -338,15 +293,6 @@ __device__ __forceinline__ TileInfo decode_tile(const FwdParams& p, int t) {
     ti.lo[1] = ti.hi[1] = 0;
   ti.lo_u = ti.lo[0];
   ti.n_u = ti.hi[0] == 0 ? 0 : max(ti.hi[0], ti.hi[1]) - ti.lo[0];
-  if constexpr (SINKS) {
-    ti.hk = p.div_group.div(ti.h);
-    ti.ns = p.window_left < 0 ? 0 : (p.sinks + BN - 1) / BN;
-    ti.gap_end = max(ti.ns, ti.lo[0]);
-    if (ti.hi[0] != 0) ti.n_u = max(ti.hi[0], ti.hi[1]) - (ti.gap_end - ti.ns);
-  } else {
-    ti.hk = ti.h;
-    ti.ns = ti.gap_end = 0;
-  }
   return ti;
 }
 
@@ -362,12 +308,10 @@ __host__ __device__ __forceinline__ int ring_v(int j, int n) { return j < n - 1 
 // j + 1, ...  Tile 0's range starts first, so it is every work tile's first
 // user.  Returns the tile of the use after (s, j), or -1 if (s, j) is the
 // work tile's last.
-template <bool SINKS>
 __device__ __forceinline__ int next_p_user(int s, int j, const TileInfo& ti) {
-  if (s == 0 && in_range<SINKS>(ti, 1, j)) return 1;
-  const int next = SINKS && j + 1 == ti.ns ? ti.gap_end : j + 1;
-  if (in_range<SINKS>(ti, 0, next)) return 0;
-  if (in_range<SINKS>(ti, 1, next)) return 1;
+  if (s == 0 && in_range(ti, 1, j)) return 1;
+  if (in_range(ti, 0, j + 1)) return 0;
+  if (in_range(ti, 1, j + 1)) return 1;
   return -1;
 }
 
@@ -419,7 +363,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------------ roles
-template <int HD, int QS, int KVS, int ELT, bool SINKS>
+template <int HD, int QS, int KVS, int ELT>
 __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
   const uint32_t bars = base + C::BAR_OFF;
@@ -447,7 +391,7 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
 #pragma unroll
     for (int c = 0; c < C::CHUNKS; ++c)
       tma_load_4d(base + C::SKV_OFF + slot * C::TILE_BYTES + c * C::CHUNK_BYTES, map, full,
-                  c * C::BOX, ti.row0 + row0, ti.hk, ti.bc);
+                  c * C::BOX, ti.row0 + row0, ti.h, ti.bc);
     ++kv_count;
     return true;
   };
@@ -467,11 +411,11 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
+    const TileInfo ti = decode_tile<QS>(p, t);
     if (ti.n_u == 0) continue;
     // The first K tile needs only a ring slot: request it before waiting for
     // the previous work tile to release the Q buffer, so the two loads overlap.
-    if (!(ok = load_kv(&p.tmap_k, block_of<SINKS>(ti, 0) * BN, ti, true))) break;
+    if (!(ok = load_kv(&p.tmap_k, ti.lo_u * BN, ti, true))) break;
     if (q_count > 0) {
       ok = wait_phase(bars + 8 * C::B_Q_EMPTY, (q_count - 1) & 1, abort_flag, p.wait_limit_ns,
                       (kRoleProducer << 8) | kSiteQEmpty);
@@ -486,14 +430,13 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
                     bars + 8 * C::B_Q_FULL, c * C::BOX, ti.row0 + ti.q0 + s * BM, ti.h, ti.bc);
     ++q_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      if (jj + 1 < ti.n_u &&
-          !(ok = load_kv(&p.tmap_k, block_of<SINKS>(ti, jj + 1) * BN, ti, true)))
-        break;
-      ok = load_kv(&p.tmap_v, block_of<SINKS>(ti, jj) * BN, ti, false);
+      const int j = ti.lo_u + jj;
+      if (jj + 1 < ti.n_u && !(ok = load_kv(&p.tmap_k, (j + 1) * BN, ti, true))) break;
+      ok = load_kv(&p.tmap_v, j * BN, ti, false);
     }
 #pragma unroll 1
     for (int s = 0; ok && s < QS; ++s)
-      if (o_via_slot<C::O_TMA && !SINKS>(p, ti, s)) ok = reserve_slot();
+      if (o_via_slot<C::O_TMA>(p, ti, s)) ok = reserve_slot();
   }
   if (!ok) {
     // Let the loads already issued land before the CTA's shared memory goes away.
@@ -520,7 +463,7 @@ __device__ void producer_role(const FwdParams& p, uint32_t base, volatile int* a
 
 // S thread, per work tile: S_s(0) for every Q tile s, then S_s(j+1) once the
 // softmax of tile s has read S_s(j) out of TMEM.
-template <int HD, int QS, int KVS, int ELT, bool SINKS>
+template <int HD, int QS, int KVS, int ELT>
 __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                            volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -573,7 +516,7 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
+    const TileInfo ti = decode_tile<QS>(p, t);
     if (ti.n_u == 0) continue;
     ok = wait_phase(bars + 8 * C::B_Q_FULL, q_count & 1, abort_flag, lim,
                     (kRoleMma << 8) | kSiteQFull);
@@ -582,17 +525,17 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
     if (!ok) break;
     const int kv0 = kv_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      const int j = block_of<SINKS>(ti, jj);
+      const int j = ti.lo_u + jj;
       const int k_idx = kv0 + ring_k(jj);
       if (!(ok = wait_kv(k_idx))) break;
 #pragma unroll 1
       for (int s = 0; s < QS; ++s)
-        if (ok && in_range<SINKS>(ti, s, j)) ok = issue_s(s, k_idx % KVS);
+        if (ok && in_range(ti, s, j)) ok = issue_s(s, k_idx % KVS);
       if (!ok) break;
       tc_commit(bars + 8 * (C::B_KV_EMPTY + k_idx % KVS));
       if (jj + 1 == ti.n_u) tc_commit(bars + 8 * C::B_Q_EMPTY);
     }
-    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
+    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
   }
   if (!ok) {
     // Wait for every MMA this thread issued before TMEM is released.
@@ -606,7 +549,7 @@ __device__ void mma_s_role(const FwdParams& p, uint32_t base, uint32_t tmem,
 // then tile 1, each once the softmax has written P_s(j) into the shared P
 // buffer; after each product the buffer is handed to the tile that uses it
 // next (which also tells that tile's softmax that O_s holds the product).
-template <int HD, int QS, int KVS, int ELT, bool SINKS>
+template <int HD, int QS, int KVS, int ELT>
 __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                             volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -657,11 +600,11 @@ __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
+    const TileInfo ti = decode_tile<QS>(p, t);
     if (ti.n_u == 0) continue;
     const int kv0 = kv_count;
     for (int jj = 0; ok && jj < ti.n_u; ++jj) {
-      const int j = block_of<SINKS>(ti, jj);
+      const int j = ti.lo_u + jj;
       const int v_idx = kv0 + ring_v(jj, ti.n_u);
       ok = wait_phase(bars + 8 * (C::B_V_FULL + v_idx % KVS), (v_par >> (v_idx % KVS)) & 1u,
                       abort_flag, lim, (kRoleMma << 8) | kSiteKvFull);
@@ -669,17 +612,17 @@ __device__ void mma_pv_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       tc_fence_after_sync();
 #pragma unroll 1
       for (int s = 0; s < QS; ++s) {
-        if (!ok || !in_range<SINKS>(ti, s, j)) continue;
+        if (!ok || !in_range(ti, s, j)) continue;
         // the next work tile starts with tile 0
-        const int nxt = next_p_user<SINKS>(s, j, ti);
-        ok = issue_pv(s, v_idx % KVS, j > first_block<SINKS>(ti, s), nxt < 0 ? 0 : nxt);
+        const int nxt = next_p_user(s, j, ti);
+        ok = issue_pv(s, v_idx % KVS, j > ti.lo[s], nxt < 0 ? 0 : nxt);
         if (!ok) break;
         if (j == ti.hi[s] - 1) tc_commit(bars + 8 * (C::B_O_FINAL + s));
       }
       if (!ok) break;
       tc_commit(bars + 8 * (C::B_KV_EMPTY + v_idx % KVS));
     }
-    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
+    kv_count = kv0 + 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
   }
   if (!ok) {
     volatile int no_abort = 0;
@@ -788,14 +731,9 @@ __device__ __forceinline__ void store_p_half_e4m3(uint32_t p_base, int r, int hf
                  pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
 }
 
-// The low n of 32 bits (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
-}
-
 // ALIBI: the scaled score of key j gets -slope[h] * |i - j| (in the log2
 // domain, -slope[h] * log2(e) * |i - j|) before the row max is taken.
-template <int HD, int QS, int KVS, int ELT, bool ALIBI, bool SINKS>
+template <int HD, int QS, int KVS, int ELT, bool ALIBI>
 __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
                              volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -841,16 +779,16 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
   for (int round = 0; round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
+    const TileInfo ti = decode_tile<QS>(p, t);
     // ring slot of this tile's O and the parity of its reservation; every
     // group follows the reservations of both tiles
     int o_slot = -1;
     uint32_t o_wait_par = 0u;
-    if (C::O_TMA && !SINKS && ti.n_u > 0) {
+    if (ti.n_u > 0) {
       int k = 0;
 #pragma unroll 1
       for (int s2 = 0; s2 < QS; ++s2) {
-        if (!o_via_slot<C::O_TMA && !SINKS>(p, ti, s2)) continue;
+        if (!o_via_slot<C::O_TMA>(p, ti, s2)) continue;
         const int slot = (kv_count + 2 * ti.n_u + k++) % KVS;
         if (s2 == s) {
           o_slot = slot;
@@ -871,8 +809,7 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
     if constexpr (ALIBI) nslope2 = -__ldg(p.alibi_slopes + ti.h) * 1.4426950408889634f;
     float m_ref = -INFINITY, l = 0.f;
 
-    const int j0 = first_block<SINKS>(ti, s);
-    for (int j = j0; j < hi; j = block_after<SINKS>(ti, s, j)) {
+    for (int j = lo; j < hi; ++j) {
       bool ok = wait_phase(bars + 8 * (C::B_S_FULL + s), s_par, abort_flag, lim,
                            (kRoleSoftmax << 8) | kSiteSFull);
       s_par ^= 1u;
@@ -888,34 +825,13 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       // tail, the causal diagonal, the edges of a local window.
       const bool need_mask =
           (j * BN + BN > ti.len) ||
-          (p.window_left >= 0 && j * BN < r_last - p.window_left &&
-           (!SINKS || j * BN + BN > p.sinks)) ||
+          (p.window_left >= 0 && j * BN < r_last - p.window_left) ||
           (p.window_right >= 0 && j * BN + BN - 1 > r_first + p.window_right);
       const int kbase = j * BN + 64 * hf;  // key of this thread's first column
-      bool none[2] = {false, false};
-      if (SINKS && need_mask) {
-        // The row's visible keys among each 32 of its 64 columns, as bits (keys
-        // past the sequence's end lie past every row's own position).  Most
-        // warps see all of 32 columns or none: the bits are only applied where
-        // they differ, and exponentials of none are not taken.
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rel = row - kbase - 32 * c;
-          uint32_t bits = low_bits(rel + 1);
-          if (p.window_left >= 0)
-            bits &= ~low_bits(rel - p.window_left) | low_bits(p.sinks - row + rel);
-          none[c] = __all_sync(0xffffffffu, bits == 0u);
-          if (!__all_sync(0xffffffffu, bits == ~0u)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              sv[32 * c + i] = (bits >> i) & 1u ? sv[32 * c + i] : -INFINITY;
-          }
-        }
-      } else if (need_mask) {
+      if (need_mask) {
         const int lo_c = vis_lo - kbase, hi_c = vis_hi - kbase;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          sv[c] = (c >= lo_c && c < hi_c) ? sv[c] : -INFINITY;
+        for (int c = 0; c < 64; ++c) sv[c] = (c >= lo_c && c < hi_c) ? sv[c] : -INFINITY;
       }
       float m_half;
       if constexpr (ALIBI) {
@@ -944,10 +860,10 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       // take the same decision from the same values.
       // A row with no visible key so far (m_ref = -inf: only possible at the
       // edges of a local window) has l = 0 and O = 0, so its alpha is 0.
-      const bool rescale = (j > j0) && (m_blk > m_ref + kLazyRescaleLog2);
-      const float m_new = (j == j0 || rescale) ? m_blk : m_ref;
+      const bool rescale = (j > lo) && (m_blk > m_ref + kLazyRescaleLog2);
+      const float m_new = (j == lo || rescale) ? m_blk : m_ref;
       const float alpha =
-          (j == j0 || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);  // 1 when m_ref is kept
+          (j == lo || m_ref == -INFINITY) ? 0.f : ex2(m_ref - m_new);  // 1 when m_ref is kept
       m_ref = m_new;
       const float neg_ref = (m_ref == -INFINITY) ? 0.f : -m_ref;
       const float sl2e = ALIBI ? 1.f : sl2;  // the ALiBi path holds scaled scores already
@@ -958,10 +874,7 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
       uint32_t pk[PK_WORDS];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (SINKS && none[c]) {
-#pragma unroll
-          for (int i = 0; i < PK_WORDS / 2; ++i) pk[(PK_WORDS / 2) * c + i] = 0u;
-        } else if (need_mask)
+        if (need_mask)
           softmax_chunk<ELT, 0>(sv + 32 * c, sl2e, neg_ref, pk + (PK_WORDS / 2) * c, acc);
         else
           softmax_chunk<ELT, poly_pairs_per8<HD>()>(sv + 32 * c, sl2e, neg_ref,
@@ -1099,7 +1012,7 @@ __device__ void softmax_role(const FwdParams& p, uint32_t base, uint32_t tmem,
 // waits until both softmax groups have staged their columns there, writes the
 // tile out with TMA stores, waits until the stores have read the slot and
 // releases it to the producer.
-template <int HD, int QS, int KVS, int ELT, bool SINKS>
+template <int HD, int QS, int KVS, int ELT>
 __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abort_flag) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
   const uint32_t bars = base + C::BAR_OFF;
@@ -1110,14 +1023,14 @@ __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abor
   for (int round = 0; ok && round * G < p.num_tiles; ++round) {
     const int t = tile_of(round, cta, G);
     if (t >= p.num_tiles) continue;
-    const TileInfo ti = decode_tile<QS, SINKS>(p, t);
+    const TileInfo ti = decode_tile<QS>(p, t);
     if (ti.n_u == 0) continue;
     const int kv0 = kv_count;
-    kv_count += 2 * ti.n_u + o_slots<C::O_TMA && !SINKS>(p, ti);
+    kv_count += 2 * ti.n_u + o_slots<C::O_TMA>(p, ti);
     int k = 0;
 #pragma unroll 1
     for (int s = 0; s < QS; ++s) {
-      if (!o_via_slot<C::O_TMA && !SINKS>(p, ti, s)) continue;
+      if (!o_via_slot<C::O_TMA>(p, ti, s)) continue;
       const int slot = (kv0 + 2 * ti.n_u + k++) % KVS;
       ok = wait_phase(bars + 8 * (C::B_O_STAGED + slot), (staged_par >> slot) & 1u, abort_flag,
                       p.wait_limit_ns, (kRoleStore << 8) | kSiteOStaged);
@@ -1137,7 +1050,7 @@ __device__ void store_role(const FwdParams& p, uint32_t base, volatile int* abor
   bulk_wait_all();
 }
 
-template <int HD, int QS, int KVS, int ELT, bool ALIBI, bool SINKS = false>
+template <int HD, int QS, int KVS, int ELT, bool ALIBI>
 __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using C = FwdCfg<HD, QS, KVS, ELT>;
@@ -1187,7 +1100,7 @@ __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
     tma_prefetch_desc(&p.tmap_q);
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
-    if (C::O_TMA && !SINKS) tma_prefetch_desc(&p.tmap_o);
+    if (C::O_TMA) tma_prefetch_desc(&p.tmap_o);
   }
   if (warp == C::MMA_S_WARP) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
@@ -1206,15 +1119,15 @@ __global__ void __launch_bounds__(FwdCfg<HD, QS, KVS, ELT>::THREADS, 1)
   }
 
   if (warp < C::SOFTMAX_WARPS) {
-    softmax_role<HD, QS, KVS, ELT, ALIBI, SINKS>(p, base, tmem, abort_flag);
+    softmax_role<HD, QS, KVS, ELT, ALIBI>(p, base, tmem, abort_flag);
   } else if (warp == C::PRODUCER_WARP) {
-    if (lane == 0) producer_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
+    if (lane == 0) producer_role<HD, QS, KVS, ELT>(p, base, abort_flag);
   } else if (warp == C::MMA_S_WARP) {
-    if (lane == 0) mma_s_role<HD, QS, KVS, ELT, SINKS>(p, base, tmem, abort_flag);
+    if (lane == 0) mma_s_role<HD, QS, KVS, ELT>(p, base, tmem, abort_flag);
   } else if (warp == C::MMA_PV_WARP) {
-    if (lane == 0) mma_pv_role<HD, QS, KVS, ELT, SINKS>(p, base, tmem, abort_flag);
+    if (lane == 0) mma_pv_role<HD, QS, KVS, ELT>(p, base, tmem, abort_flag);
   } else if (warp == C::STORE_WARP) {
-    if (lane == 0 && C::O_TMA && !SINKS) store_role<HD, QS, KVS, ELT, SINKS>(p, base, abort_flag);
+    if (lane == 0 && C::O_TMA) store_role<HD, QS, KVS, ELT>(p, base, abort_flag);
   }
 
   tc_fence_before_sync();

@@ -7,6 +7,7 @@
 #include "fa_decode.cuh"
 #include "fa_rope.cuh"
 #include "fa_sinks_bwd_sm100.cuh"
+#include "fa_sinks_fwd_sm100.cuh"
 
 namespace {
 
@@ -185,23 +186,23 @@ int check_strides(const long long* q, const long long* k, const long long* v, in
 }
 
 int encode_rows(CUtensorMap* map, const void* ptr, const long long* strides, int dtype, int d,
-                int N, int H, int B) {
+                int N, int H, int B, int rows) {
   Strides s;
   const int rc = read_strides(strides, B, H, N, d, &s);
   if (rc != FA_OK) return rc;
-  return encode_cached(map, ptr, dtype, d, N, H, B, s.n, s.h, s.b, 128);
+  return encode_cached(map, ptr, dtype, d, N, H, B, s.n, s.h, s.b, rows);
 }
 
-template <int HD, int ELT>
-int launch_fwd_sinks(const FwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
-  constexpr int QS = Pick<HD, ELT>::QS, KVS = Pick<HD, ELT>::KVS;
-  using C = FwdCfg<HD, QS, KVS, ELT>;
-  auto kernel = fa_fwd_kernel<HD, QS, KVS, ELT, false, true>;
-  const int slot = (HD == 64 ? 0 : HD == 128 ? 1 : 2) * 2 + (ELT == kBF16 ? 1 : 0);
+template <int HD, bool BF16>
+int launch_sinks_fwd(const SinksFwdParams& p, DeviceState& st, int dev, cudaStream_t stream) {
+  using C = SinksFwdCfg<HD>;
+  auto kernel = sinks_fwd_kernel<HD, BF16>;
+  const int slot = (HD == 64 ? 0 : HD == 128 ? 1 : 2) * 2 + (BF16 ? 1 : 0);
   const int rc = ensure_smem_attr(g_sinks[dev].fwd_attr[slot], kernel, C::SMEM_BYTES);
   if (rc != FA_OK) return rc;
-  const int grid = p.num_tiles < st.sm_count ? p.num_tiles : st.sm_count;
-  kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  // persistent: as many CTAs as the SMs hold at once
+  const int most = C::CTAS * st.sm_count;
+  kernel<<<p.tiles < most ? p.tiles : most, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -408,42 +409,32 @@ int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* ls
   DeviceState* st = nullptr;
   int dev = 0;
   if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
-  FwdParams p;
+  SinksFwdParams p;
   std::memset(&p, 0, sizeof(p));
-  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_o, o, nullptr, dtype, d, N, H, B)) != FA_OK)
+  constexpr int kKeys = SinksFwdCfg<128>::KEYS;
+  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B, 128)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B, kKeys)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B, kKeys)) != FA_OK)
     return rc;
   p.o = o;
   p.lse = lse;
-  p.o_stride_n = d;
-  p.o_stride_h = (long long)N * d;
-  p.o_stride_b = (long long)H * N * d;
-  p.lse_stride_b = (long long)H * N;
-  p.lse_stride_h = N;
-  p.B = B, p.H = H, p.N = N, p.rows_total = N;
-  p.causal = 1;
-  p.window_left = window;
-  p.window_right = 0;
-  p.sinks = sinks;
-  p.group = H / Hk;
+  p.B = B, p.H = H, p.N = N, p.window = window, p.sinks = sinks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  p.sink_blocks = window < 0 ? 0 : (sinks + kKeys - 1) / kKeys;
+  p.qblocks = (N + 127) / 128;
+  if ((long long)B * H * p.qblocks > 0x7fffffffLL) return FA_ERR_ARG;
+  p.tiles = B * H * p.qblocks;
   p.div_bh = FastDiv::make((uint32_t)B * H);
   p.div_h = FastDiv::make(H);
-  p.div_group = FastDiv::make(p.group);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.o_scale = 1.f;
-  p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  const int rows_per_tile = 128 * q_tiles_for(d);
-  p.num_qblocks = (N + rows_per_tile - 1) / rows_per_tile;
-  p.num_tiles = B * H * p.num_qblocks;
+  p.div_group = FastDiv::make(H / Hk);
   p.wait_limit_ns = g_wait_limit_ns.load();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == FA_BF16;
   switch (d) {
-    case 64: return bf16 ? launch_fwd_sinks<64, kBF16>(p, *st, dev, s) : launch_fwd_sinks<64, kF16>(p, *st, dev, s);
-    case 128: return bf16 ? launch_fwd_sinks<128, kBF16>(p, *st, dev, s) : launch_fwd_sinks<128, kF16>(p, *st, dev, s);
-    default: return bf16 ? launch_fwd_sinks<256, kBF16>(p, *st, dev, s) : launch_fwd_sinks<256, kF16>(p, *st, dev, s);
+    case 64: return bf16 ? launch_sinks_fwd<64, true>(p, *st, dev, s) : launch_sinks_fwd<64, false>(p, *st, dev, s);
+    case 128: return bf16 ? launch_sinks_fwd<128, true>(p, *st, dev, s) : launch_sinks_fwd<128, false>(p, *st, dev, s);
+    default: return bf16 ? launch_sinks_fwd<256, true>(p, *st, dev, s) : launch_sinks_fwd<256, false>(p, *st, dev, s);
   }
 }
 
@@ -482,10 +473,10 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
   DeviceState* st = nullptr;
   int dev = 0;
   if ((rc = device_state(&st, &dev)) != FA_OK) return rc;
-  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_do, dout, nullptr, dtype, d, N, H, B)) != FA_OK)
+  if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B, 128)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B, 128)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B, 128)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_do, dout, nullptr, dtype, d, N, H, B, 128)) != FA_OK)
     return rc;
   p.o = o;
   p.dout = dout;

@@ -37,6 +37,7 @@
 #pragma once
 
 #include "fa_bwd_sm100.cuh"
+#include "fa_sinks_fwd_sm100.cuh"
 
 namespace fa_sm100 {
 

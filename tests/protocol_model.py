@@ -34,14 +34,11 @@ class Bar:
 
 BM = BN = 128
 class P:  # params
-    def __init__(s, N, causal, QS, KVS, left=-1, right=-1, B=1, H=1, lens=None, o_tma=True,
-                 sinks=0):
+    def __init__(s, N, causal, QS, KVS, left=-1, right=-1, B=1, H=1, lens=None, o_tma=True):
         s.N, s.causal, s.QS, s.KVS = N, causal, QS, KVS
         s.wl, s.wr = left, (0 if causal else right)
         if s.wl >= N: s.wl = -1
         if s.wr >= N: s.wr = -1
-        # sinks: keys below it are visible whatever the (left) window
-        s.sink_blocks = (sinks + BN - 1) // BN if s.wl >= 0 else 0
         s.lens = lens; s.B = len(lens) if lens else B; s.H = H; s.o_tma = o_tma
         rows = 128 * QS
         s.nq = (N + rows - 1) // rows; s.num_tiles = s.B * s.H * s.nq
@@ -64,22 +61,9 @@ def decode(p, t):
     if p.QS == 2: lo[1], hi[1] = key_range(p, L, q0 + BM)
     n_u = 0 if hi[0] == 0 else max(hi[0], hi[1]) - lo[0]
     ti = dict(q0=q0, len=L, lo=lo, hi=hi, lo_u=lo[0], n_u=n_u)
-    ns = p.sink_blocks
-    if ns > 0 and n_u > 0:
-        # blocks numbered in streaming order: 0 .. ns - 1 hold the sinks, then
-        # the window's from gap_end = max(ns, lo[0]) on
-        gap = max(ns, lo[0]) - ns
-        at = lambda x: x if x <= ns else x - gap
-        ti['skip'] = [(ns, max(ns, at(max(ns, x)))) for x in lo]  # not tile s's
-        ti['hi'] = [0 if h == 0 else at(h) for h in hi]
-        ti['lo'] = [0, 0]
-        ti['lo_u'], ti['n_u'] = 0, max(ti['hi'])
     return ti
 
-def inr(ti, s, j):
-    skip = ti.get('skip')
-    if skip and skip[s][0] <= j < skip[s][1]: return False
-    return ti['lo'][s] <= j < ti['hi'][s]
+def inr(ti, s, j): return ti['lo'][s] <= j < ti['hi'][s]
 def via_slot(p, ti, s):
     if not p.o_tma or ti['lo'][s] == ti['hi'][s]: return False
     return p.lens is None or ti['q0'] + (s + 1) * BM <= ti['len']
@@ -321,7 +305,6 @@ class Sim:
             lo, hi = ti['lo'][sx], ti['hi'][sx]
             if lo == hi: continue
             for j in range(lo, hi):
-                if not inr(ti, sx, j): continue
                 s.ctx[who] = ('tile', t, 'j', j)
                 s.check_alias(f'SF{sx}', s_seen, who)
                 yield from s.wait(f'SF{sx}', spar, who); spar ^= 1; s_seen += 1
