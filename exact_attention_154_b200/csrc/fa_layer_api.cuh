@@ -414,13 +414,12 @@ int fa_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* ls
   constexpr int kKeys = SinksFwdCfg<128>::KEYS;
   if ((rc = encode_rows(&p.tmap_q, q, q_strides, dtype, d, N, H, B, 128)) != FA_OK ||
       (rc = encode_rows(&p.tmap_k, k, k_strides, dtype, d, N, Hk, B, kKeys)) != FA_OK ||
-      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B, kKeys)) != FA_OK)
+      (rc = encode_rows(&p.tmap_v, v, v_strides, dtype, d, N, Hk, B, kKeys)) != FA_OK ||
+      (rc = encode_rows(&p.tmap_o, o, nullptr, dtype, d, N, H, B, 32)) != FA_OK)
     return rc;
-  p.o = o;
   p.lse = lse;
   p.B = B, p.H = H, p.N = N, p.window = window, p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   p.sink_blocks = window < 0 ? 0 : (sinks + kKeys - 1) / kKeys;
   p.qblocks = (N + 127) / 128;
   if ((long long)B * H * p.qblocks > 0x7fffffffLL) return FA_ERR_ARG;

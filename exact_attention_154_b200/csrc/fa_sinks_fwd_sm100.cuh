@@ -25,6 +25,16 @@
 //
 // Blocks outside every row's view are neither loaded nor multiplied: a tile's
 // blocks are those holding sinks, then the window's.  Every wait is bounded.
+//
+// Measured (fp16 / bf16, d = 128, 16 query heads on 2): window 256, 4 x 4096
+// rows, 72 us; window 1024, 162 us; window 4096, 16384 rows, 560 us.  The plain
+// forward's shape given the same masks (128-key blocks, two tiles and four
+// softmax warpgroups a CTA, one CTA an SM) took 111, 178 and 519 us, and 12.2
+// against 8.1 us for 2 x 1000 rows.  A block costs a warp about 2300 cycles with
+// both CTAs at work: 800 to 1000 the exponentials (64 a row, 16 a cycle and SM),
+// 150 to 400 reading S, the rest handing over (waits that have long been
+// fulfilled, the P stores and their fence); a tile about 2000 more at its end.
+// A part of the exponentials as a polynomial on the FMA pipe was 3% slower.
 #pragma once
 
 #include "fa_fwd_sm100.cuh"
@@ -56,11 +66,10 @@ struct SinksFwdParams {
   CUtensorMap tmap_q;  // 4-D (d, N, heads, B) views, box 64 elements x 128 rows
   CUtensorMap tmap_k;  // box 64 elements x 64 rows
   CUtensorMap tmap_v;
-  void* o;             // [B, H, N, d]
+  CUtensorMap tmap_o;  // [B, H, N, d], box 64 elements x 32 rows
   float* lse;          // [B, H, N] or nullptr
   int B, H, N, window, sinks;
   float scale_log2;    // scale * log2(e)
-  int o_vec32;         // o is 32-byte aligned: 32-byte stores
   int sink_blocks;     // 64-key blocks holding sinks (0 when window < 0)
   int qblocks, tiles;  // query tiles of a head, and in all
   FastDiv div_bh, div_h, div_group;  // by B * H, H, H / Hk
@@ -133,9 +142,9 @@ template <int HD, bool BF16>
 __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t tmem,
                               volatile int* abort_flag) {
   using C = SinksFwdCfg<HD>;
-  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const uint32_t bars = base + C::BAR_OFF;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (uniform for the compiler too)
   const int r = warp * 32 + lane;  // query row within the tile == TMEM lane
   const uint32_t lane_base = tmem + ((static_cast<uint32_t>(warp) * 32u) << 16);
   const unsigned long long lim = p.wait_limit_ns;
@@ -147,33 +156,27 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
     const int t = tile_of(round, cta, G);
     if (t >= p.tiles) continue;
     const SinksTile w = sinks_tile(p, t);
-    const int row = w.q0 + r;
+    const int row0 = w.q0 + 32 * warp, row = row0 + lane;
     float m_ref = -INFINITY, l = 0.f;
     for (int jj = 0; jj < w.n; ++jj, ++blocks) {
       const int k0 = sinks_block(w, jj) * C::KEYS;
-      // The row's visible keys among each 32 of the block's 64, as bits (keys
-      // past the sequence's end lie past every row's own position); not looked
-      // for in a block that is wholly visible.  Most warps see all of 32 or
-      // none: the bits are only applied where they differ, and exponentials of
-      // none are not taken.
-      uint32_t bits[2] = {~0u, ~0u};
-      bool all = true, none[2] = {false, false};
-      if (k0 + C::KEYS - 1 > w.q0 ||
-          (p.window >= 0 && k0 < w.q0 + 127 - p.window && k0 + C::KEYS > p.sinks)) {
+      // Which keys the warp's 32 rows see, of the block and of each half of it:
+      // bounds that are the same for the whole warp (keys past the sequence's
+      // end lie past every row's own position).  Only a block that some row
+      // sees in part is masked, by bits; exponentials of a half that no row
+      // sees are not taken.
+      const bool all = k0 + C::KEYS - 1 <= row0 && (p.window < 0 || k0 >= row0 + 31 - p.window ||
+                                                    k0 + C::KEYS <= p.sinks);
+      bool none[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rel = row - k0 - 32 * c;
-          bits[c] = low_bits(rel + 1);
-          if (p.window >= 0)
-            bits[c] &= ~low_bits(rel - p.window) | low_bits(p.sinks - k0 - 32 * c);
-          none[c] = __all_sync(0xffffffffu, bits[c] == 0u);
-        }
-        all = __all_sync(0xffffffffu, (bits[0] & bits[1]) == ~0u);
+      for (int c = 0; c < 2; ++c) {
+        const int ka = k0 + 32 * c;
+        none[c] = ka > row0 + 31 || (p.window >= 0 && ka + 31 < row0 - p.window && ka >= p.sinks);
       }
       const int buf = blocks & 1;
       bool ok = wait_phase(bars + 8 * (C::B_S_FULL + buf), (blocks >> 1) & 1, abort_flag, lim,
                            (kRoleSoftmax << 8) | kSiteSFull);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      __syncwarp();  // (a wait given up is acted on below, with the next one's)
       tc_fence_after_sync();
       uint32_t sr[64];
       tmem_ld64_nowait(lane_base + C::KEYS * buf, sr);
@@ -186,6 +189,14 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
 #pragma unroll
       for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(sr[c]);
       if (!all) {
+        uint32_t bits[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rel = row - k0 - 32 * c;
+          bits[c] = low_bits(rel + 1);
+          if (p.window >= 0)
+            bits[c] &= ~low_bits(rel - p.window) | low_bits(p.sinks - k0 - 32 * c);
+        }
 #pragma unroll
         for (int c = 0; c < 64; ++c) sv[c] = (bits[c / 32] >> (c % 32)) & 1u ? sv[c] : -INFINITY;
       }
@@ -212,13 +223,14 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
       }
       const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
       l = l * alpha + ((a01.x + a23.x) + (a01.y + a23.y));
-      // The last P V has run: the P buffer is free and O holds its product.
-      if (blocks > 0) {
-        ok = wait_phase(bars + 8 * C::B_P_FREE, (blocks - 1) & 1, abort_flag, lim,
-                        (kRoleSoftmax << 8) | kSitePFree);
-        if (!__all_sync(0xffffffffu, ok)) return;
-        tc_fence_after_sync();
-      }
+      // The last P V has run: the P buffer is free (of the last tile's staged O
+      // too, once its store has read it) and O holds its product.
+      if (blocks > 0)
+        ok &= wait_phase(bars + 8 * C::B_P_FREE, (blocks - 1) & 1, abort_flag, lim,
+                         (kRoleSoftmax << 8) | kSitePFree);
+      if (jj == 0 && lane == 0) bulk_wait_read_all();
+      if (!__all_sync(0xffffffffu, ok)) return;
+      tc_fence_after_sync();
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
         for (int c = 0; c < HD; c += 16) {
@@ -246,31 +258,32 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
     if (!__all_sync(0xffffffffu, ok)) return;
     tc_fence_after_sync();
     const float inv_l = 1.f / l;
-    const bool store = row < p.N;
-    const long long at = (static_cast<long long>(w.b) * p.H + w.h) * p.N + row;
-    T* orow = static_cast<T*>(p.o) + at * HD;
+    if (p.lse != nullptr && row < p.N)
+      p.lse[(static_cast<long long>(w.b) * p.H + w.h) * p.N + row] =
+          (m_ref + log2f(l)) * 0.69314718055994530942f;
+    // 64 columns at a time through the warp's own rows of the P buffer, whose
+    // layout is the tensor map's too; rows past the sequence's end are not written
 #pragma unroll 1
     for (int c = 0; c < HD; c += 64) {
       uint32_t ov[64];
       tmem_ld64_nowait(lane_base + C::O_COL + c, ov);
       tmem_ld64_wait(ov);
-      uint4 wv[8];
-      uint32_t* wp = reinterpret_cast<uint32_t*>(wv);
+      uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        wp[i] = pack2<BF16>(__uint_as_float(ov[2 * i]) * inv_l, __uint_as_float(ov[2 * i + 1]) * inv_l);
-      if (store) {
-        if (p.o_vec32) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) st_global_v8(orow + c + 16 * i, wp + 8 * i);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = wv[i];
-        }
+        pk[i] = pack2<BF16>(__uint_as_float(ov[2 * i]) * inv_l, __uint_as_float(ov[2 * i + 1]) * inv_l);
+      if (c > 0) {
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
+      store_p_chunk(base + C::P_OFF, r, pk);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && row0 < p.N) {
+        tma_store_4d(&p.tmap_o, base + C::P_OFF + warp * 4096, c, row0, w.h, w.b);
+        bulk_commit_group();
       }
     }
-    if (p.lse != nullptr && store) p.lse[at] = (m_ref + log2f(l)) * 0.69314718055994530942f;
     tc_fence_before_sync();
   }
 }
@@ -305,6 +318,7 @@ __global__ void __launch_bounds__(SinksFwdCfg<HD>::THREADS, SinksFwdCfg<HD>::CTA
     tma_prefetch_desc(&p.tmap_q);
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
+    tma_prefetch_desc(&p.tmap_o);
   }
   if (warp == C::S_WARP) {
     tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
@@ -317,6 +331,8 @@ __global__ void __launch_bounds__(SinksFwdCfg<HD>::THREADS, SinksFwdCfg<HD>::CTA
 
   if (warp < 4) {
     sinks_softmax<HD, BF16>(p, base, tmem, abort_flag);
+    // the stores of O have read shared memory, and are complete
+    if (lane == 0) bulk_wait_all();
   } else if (warp == C::PRODUCER_WARP && lane == 0) {
     int used = 0, q_count = 0;
     bool ok = true;
