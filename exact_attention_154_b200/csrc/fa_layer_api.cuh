@@ -227,9 +227,42 @@ void sink_pieces(int N, int window, int sinks, int group, int* sink_blocks, int*
   *pieces = (nblk + *piece_blocks - 1) / *piece_blocks;
 }
 
-long long sink_part_floats(int B, int Hk, int d, int sink_blocks, int pieces) {
-  return pieces > 1 ? (long long)B * Hk * sink_blocks * pieces * 2 * 128 * d : 0;
+// How many ways the dK/dV kernel's units (key blocks and pieces, `units` in
+// all) are each split when there are few: up to one for every SM, of at least 4
+// steps, or, for the balance of long ones, up to two for every SM of at least 32.
+// Measured (us, d = 128, no split / one / two an SM): 4 heads on 1, causal, 2000
+// rows 120 / 40 / 48, 8000 rows 460 / 248 / 206; 16 heads on 2, window 256, 600
+// rows 56 / 36; at least 2 steps instead of 4: 45, 6: 34, but 2 x 8 heads on 2,
+// 500 rows, d = 64: none 34, 2: 20, 4: 19, 6: 25.
+int bwd_splits(int N, int window, int group, long long units, int piece_blocks, int sink_blocks) {
+  constexpr int kSms = 148;
+  const int nblk = (N + 127) / 128;
+  int longest = window < 0 ? nblk : (window + 127) / 128 + 2;
+  if (longest > nblk) longest = nblk;
+  if (sink_blocks > 0 && piece_blocks > longest) longest = piece_blocks;
+  const long long steps = (long long)longest * group;
+  const long long one = std::min<long long>(kSms / units, steps / 4);
+  const long long two = std::min<long long>(2 * kSms / units, steps / 32);
+  // (the kernel counts steps times splits in 31 bits)
+  const long long n = std::min(std::max(one, two), 0x7fffffffLL / steps);
+  return n > 1 ? (int)n : 1;
 }
+
+// How the work of a gradient is dealt out, and its partial sums.
+struct BwdShape {
+  int sink_blocks, pieces, piece_blocks, splits;
+  long long units, part_floats;
+  BwdShape(int B, int Hk, int group, int N, int d, int window, int sinks) {
+    sink_pieces(N, window, sinks, group, &sink_blocks, &pieces, &piece_blocks);
+    const long long heads = (long long)B * Hk, nblk = (N + 127) / 128;
+    units = heads * (sink_blocks * (long long)pieces + nblk - sink_blocks);
+    splits = bwd_splits(N, window, group, units, piece_blocks, sink_blocks);
+    const long long parts = splits > 1   ? units * splits
+                            : pieces > 1 ? heads * sink_blocks * pieces
+                                         : 0;
+    part_floats = parts * 2 * 128 * d;
+  }
+};
 
 // The dK/dV kernel is persistent, a CTA an SM.  The dQ kernel may start beside
 // it (programmatic dependent launch), filling the SMs that the dK/dV kernel's
@@ -273,13 +306,14 @@ int launch_sinks_bwd(SinksBwdParams& p, DeviceState& st, int dev, cudaStream_t s
   bwd_dsum_kernel<HD, BF16><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0,
                               stream>>>(p.o, p.dout, p.dsum, rows);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  p.units = p.B * p.Hk * (p.sink_blocks * p.pieces + p.nblk - p.sink_blocks);
+  p.units = p.B * p.Hk * (p.sink_blocks * p.pieces + p.nblk - p.sink_blocks) * p.splits;
   int rc = launch_sinks_bwd_kernel<HD, BF16, true>(p, st, dev, stream);
   if (rc != FA_OK) return rc;
   p.units = p.B * p.H * p.nblk;
   if ((rc = launch_sinks_bwd_kernel<HD, BF16, false>(p, st, dev, stream)) != FA_OK) return rc;
-  if (p.pieces > 1) {
-    const long long n = (long long)p.B * p.Hk * p.sink_blocks * 2 * 128 * (HD / 4);
+  if (p.pieces > 1 || p.splits > 1) {
+    const long long n =
+        (long long)p.B * p.Hk * (p.splits > 1 ? p.nblk : p.sink_blocks) * 2 * 128 * (HD / 4);
     sinks_sum_kernel<HD, BF16><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
@@ -442,9 +476,7 @@ long long fa_bwd_sinks_workspace(int B, int H, int Hk, int N, int d, int window,
   int rc = check_sinks(B, H, Hk, N, d, &scale, &window, &sinks, FA_BF16);
   if (rc == FA_OK && d > 128) rc = FA_ERR_HEADDIM;
   if (rc != FA_OK) return rc;
-  int sink_blocks, pieces, piece_blocks;
-  sink_pieces(N, window, sinks, H / Hk, &sink_blocks, &pieces, &piece_blocks);
-  return sink_part_floats(B, Hk, d, sink_blocks, pieces) + (long long)B * H * N;
+  return BwdShape(B, Hk, H / Hk, N, d, window, sinks).part_floats + (long long)B * H * N;
 }
 
 int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -464,10 +496,10 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
   SinksBwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.nblk = (N + 127) / 128;
-  sink_pieces(N, window, sinks, H / Hk, &p.sink_blocks, &p.pieces, &p.piece_blocks);
-  if ((long long)B * H * p.nblk > 0x7fffffffLL ||
-      (long long)B * Hk * (p.sink_blocks * (long long)p.pieces + p.nblk) > 0x7fffffffLL)
-    return FA_ERR_ARG;
+  const BwdShape shape(B, Hk, H / Hk, N, d, window, sinks);
+  if ((long long)B * H * p.nblk > 0x7fffffffLL || shape.units > 0x7fffffffLL) return FA_ERR_ARG;
+  p.sink_blocks = shape.sink_blocks, p.pieces = shape.pieces, p.piece_blocks = shape.piece_blocks;
+  p.splits = shape.splits;
   if ((rc = get_encode_fn()) != FA_OK) return rc;
   DeviceState* st = nullptr;
   int dev = 0;
@@ -481,7 +513,7 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
   p.dout = dout;
   p.lse = lse;
   p.parts = workspace;
-  p.dsum = workspace + sink_part_floats(B, Hk, d, p.sink_blocks, p.pieces);
+  p.dsum = workspace + shape.part_floats;
   p.dq = dq, p.dk = dk, p.dv = dv;
   p.out_vec32 = ((reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk) |
                   reinterpret_cast<uintptr_t>(dv)) & 31u) == 0;
@@ -490,6 +522,7 @@ int fa_bwd_sinks(const void* q, const void* k, const void* v, const void* o, con
   p.div_kv = FastDiv::make((uint32_t)B * Hk), p.div_q = FastDiv::make((uint32_t)B * H);
   p.div_hk = FastDiv::make(Hk), p.div_h = FastDiv::make(H);
   p.div_group = FastDiv::make(p.group), p.div_pieces = FastDiv::make(p.pieces);
+  p.div_splits = FastDiv::make(p.splits);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();

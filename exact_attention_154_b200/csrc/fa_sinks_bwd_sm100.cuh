@@ -14,7 +14,8 @@
 // TMEM, P^T and dS^T packed back to 16 bits there, dV += P^T dO and dK += dS^T
 // Q from TMEM.  A block that holds sinks is seen by every later query, so its
 // query blocks are dealt out as several units ("pieces") whose fp32 sums
-// sinks_sum_kernel adds.  dQ kernel: a unit is a 128-query block of a query head
+// sinks_sum_kernel adds; where units are few, all are split by their steps in the
+// same manner.  dQ kernel: a unit is a 128-query block of a query head
 // with the key blocks it sees; dQ += dS K.
 //
 // What bounds a step (128 x 128 pairs) is a chain: exponentials (the
@@ -29,6 +30,12 @@
 // in the MMA thread's order, which also is all the hand-back those columns
 // need.  The dQ kernel has no P to keep, so its S(it+1) only waits for S(it) to
 // be read, and two dP regions let dP(it+1) precede dS(it).
+//
+// Measured (bf16, d = 128): window 256, 4 x 4096 rows, 16 query heads on 2, 255
+// us (dK/dV 161, dQ beside it and after, row statistic 23, sums 7); window 2048,
+// 8205 rows, 16 heads on 4, 445 us.  A dK/dV step takes about 3400 cycles, of
+// which its four products need 2048.  Masks found from the warp's bounds and one
+// vote a step gained 2% over votes on the bits and at each wait.
 //
 // Roles, rings and the accumulators' hand-over are as in fa_bwd_sm100.cuh: 16
 // compute warps (thread = TMEM lane = tile row, warpgroup g the columns 32 g ..
@@ -64,9 +71,12 @@ struct SinksBwdParams {
   int out_vec32;       // dq, dk, dv 32-byte aligned
   int sink_blocks;     // key blocks holding sinks (0 when window < 0)
   int pieces, piece_blocks;  // of a sink block: pieces of that many query blocks
-  float* parts;        // pieces > 1: fp32 [B, Hk, sink_blocks, pieces, {dV, dK}, 128, d]
+  int splits;          // of the steps of each dK/dV unit, when there are few units
+  // pieces or splits > 1: fp32 [part, {dV, dK}, 128, d], parts numbered (B, Hk, sink
+  // block, piece, split), then, with splits > 1, (B, Hk, other key block, split)
+  float* parts;
   unsigned long long wait_limit_ns;
-  FastDiv div_kv, div_q, div_hk, div_h, div_group, div_pieces;  // by B Hk, B H, Hk, H, group, pieces
+  FastDiv div_kv, div_q, div_hk, div_h, div_group, div_pieces, div_splits;
 };
 
 template <int HD, bool KV>
@@ -129,15 +139,37 @@ struct SinksUnit {
   int first, per_head;  // dK/dV: query blocks first .. first + per_head - 1 of each head
   int ns, gap_end;    // dQ: key blocks 0 .. ns - 1, then gap_end on
   int count;          // streamed steps
+  int start;          // dK/dV: the first of them among its query blocks of all heads
   int h0;             // first streamed head
   int part;           // dK/dV: this piece's partial sums, or -1
 };
 
-// Query blocks [first, end) of piece `piece` of sink block blk.
-__device__ __forceinline__ void sink_piece(const SinksBwdParams& p, int blk, int piece, int* first,
-                                           int* end) {
-  *first = min(p.nblk, blk + piece * p.piece_blocks);
-  *end = min(p.nblk, *first + p.piece_blocks);
+// Query blocks [first, end) that see key block blk; of a sink block, those of
+// one piece.
+__device__ __forceinline__ void key_block_queries(const SinksBwdParams& p, int blk, int piece,
+                                                  int* first, int* end) {
+  if (blk < p.sink_blocks) {
+    *first = min(p.nblk, blk + piece * p.piece_blocks);
+    *end = min(p.nblk, *first + p.piece_blocks);
+  } else {
+    // those with a row at most `window` past the block's last key
+    *first = blk;
+    *end = p.window < 0 ? p.nblk
+                        : static_cast<int>(min(static_cast<long long>(p.nblk),
+                                               (blk * 128ll + 127 + p.window) / 128 + 1));
+  }
+}
+
+// First of the steps of split i (the steps dealt out as evenly as they go).
+__device__ __forceinline__ int split_start(const SinksBwdParams& p, int steps, int i) {
+  return p.div_splits.div(steps * i);
+}
+
+// Where the partial sums of (b, key head) bh's key block blk begin.
+__device__ __forceinline__ int first_part(const SinksBwdParams& p, int bh, int blk) {
+  if (blk < p.sink_blocks) return (bh * p.sink_blocks + blk) * p.pieces * p.splits;
+  return (p.B * p.Hk * p.sink_blocks * p.pieces + bh * (p.nblk - p.sink_blocks) + blk -
+          p.sink_blocks) * p.splits;
 }
 
 // Units with the most blocks first: the sink blocks' pieces, then the other key
@@ -146,31 +178,30 @@ template <bool KV>
 __device__ __forceinline__ SinksUnit sinks_unit(const SinksBwdParams& p, int u) {
   SinksUnit w;
   const int nh = KV ? p.Hk : p.H, heads = p.B * nh;
-  const int rank = (KV ? p.div_kv : p.div_q).div(u);
+  int rank = (KV ? p.div_kv : p.div_q).div(u);
   w.bh = u - rank * heads;
   w.b = (KV ? p.div_hk : p.div_h).div(w.bh);
   w.h = w.bh - w.b * nh;
   w.part = -1;
+  w.start = 0;
   if (KV) {
     w.h0 = w.h * p.group;
     w.ns = w.gap_end = 0;
+    const int sub = p.splits > 1 ? rank - p.div_splits.div(rank) * p.splits : 0;
+    if (p.splits > 1) rank = p.div_splits.div(rank);
+    const int sink_units = p.sink_blocks * p.pieces;
+    w.blk = rank < sink_units ? p.div_pieces.div(rank) : p.sink_blocks + rank - sink_units;
+    const int piece = rank < sink_units ? rank - w.blk * p.pieces : 0;
     int end;
-    const int split = p.sink_blocks * p.pieces;
-    if (rank < split) {
-      w.blk = p.div_pieces.div(rank);
-      const int piece = rank - w.blk * p.pieces;
-      sink_piece(p, w.blk, piece, &w.first, &end);
-      if (p.pieces > 1) w.part = (w.bh * p.sink_blocks + w.blk) * p.pieces + piece;
-    } else {
-      w.blk = p.sink_blocks + rank - split;
-      w.first = w.blk;
-      // query blocks with a row at most `window` past the block's last key
-      end = p.window < 0 ? p.nblk
-                         : static_cast<int>(min(static_cast<long long>(p.nblk),
-                                                (w.blk * 128ll + 127 + p.window) / 128 + 1));
-    }
+    key_block_queries(p, w.blk, piece, &w.first, &end);
     w.per_head = end - w.first;
     w.count = w.per_head * p.group;
+    if (p.splits > 1 || (rank < sink_units && p.pieces > 1))
+      w.part = first_part(p, w.bh, w.blk) + piece * p.splits + sub;
+    if (p.splits > 1) {
+      w.start = split_start(p, w.count, sub);
+      w.count = split_start(p, w.count, sub + 1) - w.start;
+    }
   } else {
     w.blk = p.nblk - 1 - rank;
     w.h0 = p.div_group.div(w.h);
@@ -190,6 +221,7 @@ struct SinksStep {
   __device__ __forceinline__ explicit SinksStep(const SinksUnit& w) {
     h = w.h0;
     blk = KV ? w.first : w.ns == 0 ? w.gap_end : 0;
+    if (KV && w.start > 0) h += w.start / w.per_head, blk += w.start % w.per_head;
   }
   __device__ __forceinline__ void next(const SinksUnit& w) {
     ++blk;
@@ -198,8 +230,8 @@ struct SinksStep {
   }
 };
 
-// Writes NC fp32 columns of row r of dV (a0) and dK (a1) of one piece of a
-// sink block to its partial sums.
+// Writes NC fp32 columns of row r of dV (a0) and dK (a1) of one piece or split
+// of a key block to its partial sums.
 template <int NC>
 __device__ __forceinline__ void store_part(float* parts, int part, int hd, int r, int c,
                                            const uint32_t* a0, const uint32_t* a1) {
@@ -423,7 +455,8 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
     }
   } else {
     // compute warps: thread = tile row = TMEM lane; this warpgroup's columns
-    const int quad = warp % 4, grp = warp / 4, cb = 32 * grp;
+    const int uw = __shfl_sync(0xffffffffu, warp, 0);  // (uniform for the compiler too)
+    const int quad = uw % 4, grp = uw / 4, cb = 32 * grp;
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((static_cast<uint32_t>(quad) * 32u) << 16);
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
@@ -435,7 +468,8 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
       if (u >= p.units) continue;
       const SinksUnit w = sinks_unit<KV>(p, u);
       if (w.count <= 0) continue;
-      const int my_row = w.blk * 128 + r;  // key row (dK/dV) or query row (dQ)
+      const int row0 = w.blk * 128 + 32 * quad;
+      const int my_row = row0 + lane;  // key row (dK/dV) or query row (dQ)
       // Statistics are kept as loaded: scaling them here would wait for the load.
       float my_lse = INFINITY, my_d = 0.f;  // dQ: LSE and D of the row
       if (!KV && my_row < p.N) {
@@ -465,24 +499,14 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         // see all of their columns or none, so the bits are only applied where
         // they differ, and not even looked for in a block that is wholly visible
         // (below the diagonal, inside the window).
-        uint32_t bits = ~0u;
-        bool all = true, none = false;
-        const int ahead = (KV ? st.blk - w.blk : w.blk - st.blk) * 128;  // of the query block
-        if (ahead < 128 || (p.window >= 0 && ahead + 127 > p.window)) {
-          const int rel = my_row - st.blk * 128 - cb;
-          if (KV) {
-            bits = ~low_bits(rel);
-            if (p.window >= 0 && my_row >= p.sinks) bits &= low_bits(rel + p.window + 1);
-          } else {
-            bits = low_bits(rel + 1);
-            if (p.window >= 0) bits &= ~low_bits(rel - p.window) | low_bits(p.sinks - st.blk * 128 - cb);
-          }
-          all = __all_sync(0xffffffffu, bits == ~0u);
-          none = __all_sync(0xffffffffu, bits == 0u);
-        }
+        const int q_lo = KV ? st.blk * 128 + cb : row0, k_lo = KV ? row0 : st.blk * 128 + cb;
+        const bool all = k_lo + 31 <= q_lo &&
+                         (p.window < 0 || q_lo + 31 - k_lo <= p.window || k_lo + 32 <= p.sinks);
+        const bool none = k_lo > q_lo + 31 ||
+                          (p.window >= 0 && q_lo - k_lo - 31 > p.window && k_lo >= p.sinks);
         ok = wait_phase(bars + 8 * C::B_S_FULL, gs & 1, abort_flag, lim,
                         (kRoleSoftmax << 8) | kSiteSFull);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        __syncwarp();  // (a wait given up is acted on below, with the next one's)
         tc_fence_after_sync();
         // P, kept in fp32
         float2 pv[16];
@@ -521,6 +545,16 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
             pv[q] = make_float2(ex2(x.x), ex2(x.y));
           }
           if (!all) {
+            const int rel = my_row - st.blk * 128 - cb;
+            uint32_t bits;
+            if (KV) {
+              bits = ~low_bits(rel);
+              if (p.window >= 0 && my_row >= p.sinks) bits &= low_bits(rel + p.window + 1);
+            } else {
+              bits = low_bits(rel + 1);
+              if (p.window >= 0)
+                bits &= ~low_bits(rel - p.window) | low_bits(p.sinks - st.blk * 128 - cb);
+            }
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
               pv[q].x = (bits >> (2 * q)) & 1u ? pv[q].x : 0.f;
@@ -543,8 +577,8 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         st.next(w);
         if (KV && it + 1 < w.count) load_stats();
         // dS = P (dP - D)
-        ok = wait_phase(bars + 8 * C::step_bar(C::B_DP_FULL, gs), C::step_parity(gs), abort_flag,
-                        lim, (kRoleSoftmax << 8) | kSiteSFull);
+        ok &= wait_phase(bars + 8 * C::step_bar(C::B_DP_FULL, gs), C::step_parity(gs), abort_flag,
+                         lim, (kRoleSoftmax << 8) | kSiteSFull);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after_sync();
         const uint32_t dpc = C::dp_col(gs);
@@ -619,37 +653,44 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
   }
 }
 
-// dV and dK of the sink blocks: the pieces' partial sums added in order, dK
-// times the scale, rounded once.  A thread takes 4 columns of one row.
+// dV and dK of the key blocks that were dealt out (the sink blocks', or all with
+// splits > 1): the partial sums added in order, dK times the scale, rounded
+// once.  A thread takes 4 columns of one row.
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(256) sinks_sum_kernel(const __grid_constant__ SinksBwdParams p) {
   constexpr int C4 = HD / 4;
-  const long long n = static_cast<long long>(p.B) * p.Hk * p.sink_blocks * 2 * 128 * C4;
+  const int blocks = p.splits > 1 ? p.nblk : p.sink_blocks;  // of a head
+  const long long n = static_cast<long long>(p.B) * p.Hk * blocks * 2 * 128 * C4;
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
   const int c = static_cast<int>(i % C4) * 4;
   const int r = static_cast<int>(i / C4 % 128);
   const int which = static_cast<int>(i / (C4 * 128) % 2);  // 0: dV, 1: dK
-  const long long block = i / (C4 * 128 * 2);
-  const int blk = static_cast<int>(block % p.sink_blocks);
-  const long long bh = block / p.sink_blocks;
+  const int block = static_cast<int>(i / (C4 * 128 * 2));
+  const int bh = block / blocks, blk = block - bh * blocks;
   const int row = blk * 128 + r;
   if (row >= p.N) return;
+  const int pieces = blk < p.sink_blocks ? p.pieces : 1;
+  const float* at = p.parts + ((first_part(p, bh, blk) * 2ll + which) * 128 + r) * HD + c;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int piece = 0; piece < p.pieces; ++piece) {
+  for (int piece = 0; piece < pieces; ++piece) {
     int first, end;
-    sink_piece(p, blk, piece, &first, &end);
-    if (first >= end) break;
-    const float4 v = __ldg(reinterpret_cast<const float4*>(
-        p.parts + (((block * p.pieces + piece) * 2 + which) * 128 + r) * HD + c));
-    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    key_block_queries(p, blk, piece, &first, &end);
+    const int steps = (end - first) * p.group;
+#pragma unroll 4
+    for (int sub = 0; sub < p.splits; ++sub, at += 2 * 128 * HD) {
+      // (a piece past the sequence's end or a split without a step has no sums)
+      if (p.splits == 1 ? steps <= 0 : split_start(p, steps, sub) == split_start(p, steps, sub + 1))
+        continue;
+      const float4 v = __ldg(reinterpret_cast<const float4*>(at));
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
   }
   const float mul = which ? p.scale : 1.f;
   uint2 w = make_uint2(pack2<BF16>(t.x * mul, t.y * mul), pack2<BF16>(t.z * mul, t.w * mul));
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   T* out = static_cast<T*>(which ? p.dk : p.dv);
-  *reinterpret_cast<uint2*>(out + (bh * p.N + row) * HD + c) = w;
+  *reinterpret_cast<uint2*>(out + (static_cast<long long>(bh) * p.N + row) * HD + c) = w;
 }
 
 }  // namespace fa_sm100

@@ -26,11 +26,11 @@
 // Blocks outside every row's view are neither loaded nor multiplied: a tile's
 // blocks are those holding sinks, then the window's.  Every wait is bounded.
 //
-// Measured (fp16 / bf16, d = 128, 16 query heads on 2): window 256, 4 x 4096
-// rows, 72 us; window 1024, 162 us; window 4096, 16384 rows, 560 us.  The plain
-// forward's shape given the same masks (128-key blocks, two tiles and four
-// softmax warpgroups a CTA, one CTA an SM) took 111, 178 and 519 us, and 12.2
-// against 8.1 us for 2 x 1000 rows.  A block costs a warp about 2300 cycles with
+// Measured (bf16, d = 128, 16 query heads on 2): window 256, 4 x 4096 rows,
+// 72 us; window 1024, 162 us; window 4096, 16384 rows, 560 us; 2 x 12 heads of
+// 333 rows at d = 64, 8.1 us.  The plain forward's shape given the same masks
+// (128-key blocks, two tiles and four softmax warpgroups a CTA, one CTA an SM)
+// took 111, 178, 519 and 12.2 us.  A block costs a warp about 2300 cycles with
 // both CTAs at work: 800 to 1000 the exponentials (64 a row, 16 a cycle and SM),
 // 150 to 400 reading S, the rest handing over (waits that have long been
 // fulfilled, the P stores and their fence); a tile about 2000 more at its end.

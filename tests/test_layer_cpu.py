@@ -188,10 +188,16 @@ def test_sinks_argument_errors(lib):
 
 def test_sinks_workspace(lib):
     w = lib.fa_bwd_sinks_workspace
+    # 2 x 2 key heads of 3 blocks: 6 steps at most, not split; 4 heads a group
+    # and 12 steps: in 3
     assert w(2, 4, 2, 300, 128, -1, 4) == 2 * 4 * 300
-    assert w(2, 4, 2, 300, 128, 64, 0) == 2 * 4 * 300
-    # 32 blocks, shares of 4: one sink block in 8 pieces of [2, 128, d]
+    assert w(2, 8, 2, 300, 128, 64, 0) == 2 * 8 * 300 + 2 * 2 * 3 * 3 * 2 * 128 * 128
+    # 32 blocks, shares of 4: one sink block in 8 pieces of [2, 128, d]; 156 units
     assert w(2, 4, 2, 4096, 64, 256, 4) == 2 * 4 * 4096 + 2 * 2 * 8 * 2 * 128 * 64
+    # one key head of 63 blocks, 252 steps: in 4
+    assert w(1, 4, 1, 8000, 128, -1, 0) == 4 * 8000 + 63 * 4 * 2 * 128 * 128
+    # an extreme group: steps times splits stay below 2^31
+    assert w(1, 1 << 26, 1, 1, 64, -1, 0) == (1 << 26) + 31 * 2 * 128 * 64
     assert w(1, 4, 3, 300, 128, 64, 0) == fa.FA_ERR_ARG
     assert w(1, 4, 2, 300, 256, 64, 0) == fa.FA_ERR_HEADDIM
 
@@ -199,10 +205,12 @@ def test_sinks_workspace(lib):
 @pytest.mark.parametrize("N,window,sinks", [(1, -1, 0), (900, -1, 0), (900, 0, 0), (900, 0, 1),
                                             (1000, 100, 4), (4096, 256, 4), (4096, 256, 300),
                                             (3000, 130, 1500), (2049, 1, 128), (5000, 2047, 16)])
-def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks):
-    """The dK/dV and dQ kernels' units (fa_bwd_sm100.cuh sinks_unit, restated)
-    against the mask, by blocks: every visible pair of blocks once for each
-    query head, none twice."""
+@pytest.mark.parametrize("splits", [1, 2, 5, 37])
+def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks, splits):
+    """The dK/dV and dQ kernels' units (fa_sinks_bwd_sm100.cuh sinks_unit,
+    restated) against the mask, by blocks: every visible pair of blocks once for
+    each query head, none twice; and the partial sums, each written once and
+    read by the sum kernel's order of them."""
     B, H, G = 1, 4, 2
     Hk, nblk = H // G, (N + 127) // 128
     W = -1 if window >= N - 1 else window
@@ -214,9 +222,16 @@ def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks):
         if want > 1:
             size = -(-nblk // want)
             pieces = -(-nblk // size)
-    pairs = []
-    for u in range(B * Hk * (ns * pieces + nblk - ns)):
+    def first_part(hk, blk):
+        if blk < ns:
+            return (hk * ns + blk) * pieces * splits
+        return (B * Hk * ns * pieces + hk * (nblk - ns) + blk - ns) * splits
+
+    pairs, written = [], {}
+    for u in range(B * Hk * (ns * pieces + nblk - ns) * splits):
         rank, hk = divmod(u, B * Hk)
+        rank, sub = divmod(rank, splits)
+        piece = 0
         if rank < ns * pieces:
             blk, piece = divmod(rank, pieces)
             first = min(nblk, blk + piece * size)
@@ -225,8 +240,28 @@ def test_gradient_units_cover_every_visible_block_pair_once(N, window, sinks):
             blk = first = ns + rank - ns * pieces
             end = nblk if W < 0 else min(nblk, (blk * 128 + 127 + W) // 128 + 1)
         per = end - first
-        for it in range(per * G):
-            pairs.append((hk * G + it // per, first + it % per, blk))
+        lo, hi = per * G * sub // splits, per * G * (sub + 1) // splits
+        # the kernel's iterator, started inside a head's query blocks
+        h, q = (hk * G + lo // per, first + lo % per) if per else (0, 0)
+        for _ in range(hi - lo):
+            pairs.append((h, q, blk))
+            q += 1
+            if q == first + per:
+                q, h = first, h + 1
+        if hi > lo and (splits > 1 or (pieces > 1 and blk < ns)):
+            part = first_part(hk, blk) + piece * splits + sub
+            assert part not in written
+            written[part] = (hk, blk)
+    read = {}
+    for hk in range(Hk):
+        for blk in range(nblk if splits > 1 else ns if pieces > 1 else 0):
+            np_ = pieces if blk < ns else 1
+            for i in range(np_ * splits):
+                part = first_part(hk, blk) + i
+                assert part not in read
+                read[part] = (hk, blk)
+    assert written.items() <= read.items()
+    assert len(read) <= B * Hk * (ns * pieces + nblk - ns) * splits and max(read, default=-1) < max(1, len(read))
     dq = []
     for u in range(B * H * nblk):
         rank, h = divmod(u, B * H)

@@ -100,9 +100,12 @@ def test_gradient(window, sinks, dtype, d):
 
 
 @pytest.mark.parametrize("case", [(1, 8, 1, 2500, 128, 300, 130), (2, 6, 3, 2100, 64, 100, 4),
-                                  (1, 40, 8, 700, 128, 150, 1)])
+                                  (1, 40, 8, 700, 128, 150, 1), (2, 24, 24, 400, 64, 100, 0),
+                                  (3, 30, 10, 640, 128, 200, 4), (1, 4, 1, 2000, 128, -1, 0),
+                                  (2, 8, 2, 500, 64, 256, 4), (2, 20, 2, 1500, 64, 500, 200)])
 def test_many_units_and_split_sinks(case):
-    """More work tiles and units than SMs, sink blocks split into pieces."""
+    """More work tiles and units than SMs; sink blocks split into pieces; the
+    few units of small problems split by their steps."""
     B, H, Hk, N, d, window, sinks = case
     q, k, v = qkv(B, H, Hk, N, d, torch.bfloat16, 400 + N)
     dout, o, lse, got = check_bwd(q, k, v, window, sinks, 401, scale=0.1)
@@ -123,7 +126,8 @@ def test_unbounded_window_is_the_plain_causal_problem():
             torch.cuda.synchronize()
             check_fwd(q, k, v, -1, 0, *got)
             assert window == 0 or (torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]))
-        if d < 256:
+        if d < 256:  # 192 units of 128 keys: none is split, so the sums' order is the same
+            q, k, v = qkv(2, 24, 24, 400, d, torch.bfloat16, 600 + d)
             ref, g = fa.fwd(q, k, v, causal=True), torch.randn_like(q)
             for a, b in zip(fa.bwd_sinks(q, k, v, *ref, g, -1, 0), fa.bwd(q, k, v, *ref, g, causal=True)):
                 assert torch.equal(a, b)
