@@ -190,7 +190,7 @@ int encode_rows(CUtensorMap* map, const void* ptr, const long long* strides, int
   Strides s;
   const int rc = read_strides(strides, B, H, N, d, &s);
   if (rc != FA_OK) return rc;
-  return encode_cached(map, ptr, dtype, d, N, H, B, s.n, s.h, s.b, rows);
+  return encode_operand(map, ptr, dtype, d, N, H, B, s.n, s.h, s.b, rows);
 }
 
 template <int HD, bool BF16>
@@ -418,8 +418,8 @@ int fa_decode_sinks(const void* q, const void* k, const void* v, void* o, float*
   std::memset(&p, 0, sizeof(p));
   p.q = q, p.o = o, p.lse = lse, p.seqlens = seqlens;
   const int keys = d == 256 ? DecodeCfg<256, 1>::KEYS : DecodeCfg<128, 1>::KEYS;  // of a step
-  if ((rc = encode_cached(&p.tmap_k, k, dtype, d, S, Hk, B, ks.n, ks.h, ks.b, keys)) != FA_OK ||
-      (rc = encode_cached(&p.tmap_v, v, dtype, d, S, Hk, B, vs.n, vs.h, vs.b, keys)) != FA_OK)
+  if ((rc = encode_operand(&p.tmap_k, k, dtype, d, S, Hk, B, ks.n, ks.h, ks.b, keys)) != FA_OK ||
+      (rc = encode_operand(&p.tmap_v, v, dtype, d, S, Hk, B, vs.n, vs.h, vs.b, keys)) != FA_OK)
     return rc;
   p.H = H, p.Hk = Hk, p.S = S, p.window = window, p.sinks = sinks, p.group = H / Hk;
   p.scale_log2 = scale * 1.4426950408889634f;

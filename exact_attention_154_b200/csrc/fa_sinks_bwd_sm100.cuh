@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(SinksBwdCfg<HD, KV>::THREADS, 1)
         // dS = P (dP - D)
         ok &= wait_phase(bars + 8 * C::step_bar(C::B_DP_FULL, gs), C::step_parity(gs), abort_flag,
                          lim, (kRoleSoftmax << 8) | kSiteSFull);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after_sync();
         const uint32_t dpc = C::dp_col(gs);
         tmem_ld32_sync(lane_base + dpc + cb, sv);
