@@ -14,11 +14,14 @@
 // small and independent, and two CTAs share an SM (d <= 128): one computes
 // while the other starts, ends or waits.  One warpgroup owns a tile's rows
 // whole (thread = row = TMEM lane, 64 columns a block), so row maxima and sums
-// need no exchange; S has two buffers, so the next block's scores are there
-// when its turn comes, whatever P V is doing.
+// need no exchange.  P is packed over the scores it came from, in TMEM: the
+// shared-memory port, which feeds the products and takes the loads, would have
+// 32 of its 128 KB a block more to move with P there (window 256 83 -> 77 us, 4096
+// 560 -> 518, short 10.2 -> 8.6).  S has two buffers, so the next block's scores
+// are there when its turn comes: S(j+1) only waits for P(j-1) V.
 //
-//   warps 0-3  softmax: S from TMEM, mask, exponentials, P to shared memory,
-//              O rescaled in TMEM when the reference moves, O / l written out
+//   warps 0-3  softmax: S from TMEM, mask, exponentials, P back over S, O
+//              rescaled in TMEM when the reference moves, O / l written out
 //   warp 4     TMA: Q once a tile, K and V blocks through a ring
 //   warp 5, 6  one thread each issues S = Q K^T and O += P V (a thread that
 //              issues MMAs runs only about one instruction ahead of the pipe)
@@ -83,20 +86,19 @@ struct SinksFwdCfg {
   static constexpr int CHUNKS = HD / 64;             // 128-byte columns of a row
   static constexpr int Q_CHUNK = 128 * 128, KV_CHUNK = KEYS * 128;
   static constexpr int Q_BYTES = CHUNKS * Q_CHUNK, KV_BYTES = CHUNKS * KV_CHUNK;
-  static constexpr int P_BYTES = 128 * KEYS * 2;
+  static constexpr int O_BYTES = 128 * 64 * 2;       // 64 columns of O on their way out
   static constexpr int RING = HD == 64 ? 8 : 4;      // K or V blocks
   static constexpr int CTAS = HD == 256 ? 1 : 2;     // of an SM
   static constexpr int WARPS = 7, THREADS = 32 * WARPS;
   static constexpr int PRODUCER_WARP = 4, S_WARP = 5, PV_WARP = 6;
-  static constexpr int Q_OFF = 0, P_OFF = Q_BYTES, RING_OFF = P_OFF + P_BYTES;
+  static constexpr int Q_OFF = 0, O_OFF = Q_BYTES, RING_OFF = O_OFF + O_BYTES;
   static constexpr int BAR_OFF = RING_OFF + RING * KV_BYTES;
   // A ring slot holds K or V blocks in turn, each completing on a barrier of
   // its own consumer, so that every barrier's phases are waited in order.
   static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_K_FULL = 2, B_V_FULL = B_K_FULL + RING,
                        B_EMPTY = B_V_FULL + RING, B_S_FULL = B_EMPTY + RING /* [2] */,
-                       B_S_FREE = B_S_FULL + 2 /* [2] */, B_P_FULL = B_S_FREE + 2,
-                       B_P_FREE = B_P_FULL + 1, B_O_FINAL = B_P_FREE + 1, B_DRAIN = B_O_FINAL + 1,
-                       NUM_BARS = B_DRAIN + 2;
+                       B_P_FULL = B_S_FULL + 2 /* [2] */, B_S_FREE = B_P_FULL + 2 /* [2] */,
+                       B_O_FINAL = B_S_FREE + 2, B_DRAIN = B_O_FINAL + 1, NUM_BARS = B_DRAIN + 2;
   static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
   static constexpr int END_OFF = MISC_OFF + 16;
   // shared memory of a CTA (228 KB an SM, 1 KB of each CTA's reserved); what is
@@ -105,7 +107,7 @@ struct SinksFwdCfg {
   static constexpr int SLACK = LIMIT - END_OFF < 1008 ? LIMIT - END_OFF : 1008;
   static constexpr int SMEM_BYTES = END_OFF + SLACK;
   static_assert(SLACK >= 0, "shared memory budget");
-  // TMEM columns: two S buffers, O
+  // TMEM columns: two S buffers (P over the first half of its S), O
   static constexpr uint32_t O_COL = 2 * KEYS;
   static constexpr uint32_t TMEM_COLS = HD == 256 ? 512 : 256;
   static_assert(O_COL + HD <= TMEM_COLS, "TMEM budget");
@@ -181,10 +183,6 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
       uint32_t sr[64];
       tmem_ld64_nowait(lane_base + C::KEYS * buf, sr);
       tmem_ld64_wait(sr);
-      // S is in registers: the buffer may take the scores after the next
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (C::B_S_FREE + buf));
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(sr[c]);
@@ -223,15 +221,15 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
       }
       const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
       l = l * alpha + ((a01.x + a23.x) + (a01.y + a23.y));
-      // The last P V has run: the P buffer is free (of the last tile's staged O
-      // too, once its store has read it) and O holds its product.
-      if (blocks > 0)
-        ok &= wait_phase(bars + 8 * C::B_P_FREE, (blocks - 1) & 1, abort_flag, lim,
-                         (kRoleSoftmax << 8) | kSitePFree);
-      if (jj == 0 && lane == 0) bulk_wait_read_all();
+      // O is only touched where the reference moved, once the last P V has run
+      // (which hands back the other buffer)
+      const bool move = __any_sync(0xffffffffu, rescale);
+      if (move)
+        ok &= wait_phase(bars + 8 * (C::B_S_FREE + (buf ^ 1)), ((blocks - 1) >> 1) & 1, abort_flag,
+                         lim, (kRoleSoftmax << 8) | kSitePFree);
       if (!__all_sync(0xffffffffu, ok)) return;
-      tc_fence_after_sync();
-      if (__any_sync(0xffffffffu, rescale)) {
+      if (move) {
+        tc_fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < HD; c += 16) {
           uint32_t ov[16];
@@ -240,14 +238,13 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
           for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
           tmem_st16(lane_base + C::O_COL + c, ov);
         }
-        tmem_st_wait();
       }
-      store_p_chunk(base + C::P_OFF, r, pk);
-      // make the generic-proxy stores visible to the tensor core
-      fence_proxy_async_smem();
+      // P, two keys a column, over the scores just read
+      tmem_st32(lane_base + C::KEYS * buf, pk);
+      tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * C::B_P_FULL);
+      if (lane == 0) mbar_arrive(bars + 8 * (C::B_P_FULL + buf));
     }
 
     // O / l and the logsumexp, once the tile's last P V has run.  The next
@@ -261,8 +258,8 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
     if (p.lse != nullptr && row < p.N)
       p.lse[(static_cast<long long>(w.b) * p.H + w.h) * p.N + row] =
           (m_ref + log2f(l)) * 0.69314718055994530942f;
-    // 64 columns at a time through the warp's own rows of the P buffer, whose
-    // layout is the tensor map's too; rows past the sequence's end are not written
+    // 64 columns at a time through the warp's own rows of the staging buffer, in
+    // the tensor map's layout; rows past the sequence's end are not written
 #pragma unroll 1
     for (int c = 0; c < HD; c += 64) {
       uint32_t ov[64];
@@ -272,15 +269,13 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         pk[i] = pack2<BF16>(__uint_as_float(ov[2 * i]) * inv_l, __uint_as_float(ov[2 * i + 1]) * inv_l);
-      if (c > 0) {
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
-      }
-      store_p_chunk(base + C::P_OFF, r, pk);
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+      store_p_chunk(base + C::O_OFF, r, pk);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && row0 < p.N) {
-        tma_store_4d(&p.tmap_o, base + C::P_OFF + warp * 4096, c, row0, w.h, w.b);
+        tma_store_4d(&p.tmap_o, base + C::O_OFF + warp * 4096, c, row0, w.h, w.b);
         bulk_commit_group();
       }
     }
@@ -310,7 +305,7 @@ __global__ void __launch_bounds__(SinksFwdCfg<HD>::THREADS, SinksFwdCfg<HD>::CTA
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NUM_BARS; ++i)
-      mbar_init(bars + 8 * i, (i >= C::B_S_FREE && i <= C::B_P_FULL) ? 4 : 1);  // a softmax warp each
+      mbar_init(bars + 8 * i, (i >= C::B_P_FULL && i < C::B_S_FREE) ? 4 : 1);  // a softmax warp each
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -438,7 +433,6 @@ __global__ void __launch_bounds__(SinksFwdCfg<HD>::THREADS, SinksFwdCfg<HD>::CTA
     }
   } else if (warp == C::PV_WARP && lane == 0) {
     const uint32_t idesc = f16_idesc(BF16, 128, HD, true);
-    const uint32_t pa = sw128_desc_lo(base + C::P_OFF, 16);
     int used = 0, blocks = 0;
     uint32_t v_par = 0u;
     bool ok = true;
@@ -447,21 +441,21 @@ __global__ void __launch_bounds__(SinksFwdCfg<HD>::THREADS, SinksFwdCfg<HD>::CTA
       if (t >= p.tiles) continue;
       const int n = sinks_tile(p, t).n;
       for (int jj = 0; ok && jj < n; ++jj, ++blocks) {
-        const int slot = (used + ring_v(jj, n)) % C::RING;
+        const int slot = (used + ring_v(jj, n)) % C::RING, buf = blocks & 1;
         if (!(ok = wait_phase(bars + 8 * (C::B_V_FULL + slot), (v_par >> slot) & 1u, abort_flag, lim,
                               (kRoleMma << 8) | kSiteKvFull)))
           break;
         v_par ^= 1u << slot;
-        if (!(ok = wait_phase(bars + 8 * C::B_P_FULL, blocks & 1, abort_flag, lim,
+        if (!(ok = wait_phase(bars + 8 * (C::B_P_FULL + buf), (blocks >> 1) & 1, abort_flag, lim,
                               (kRoleMma << 8) | kSitePFull)))
           break;
         tc_fence_after_sync();
         const uint32_t vb = sw128_desc_lo(base + C::RING_OFF + slot * C::KV_BYTES, C::KV_CHUNK);
 #pragma unroll
         for (int kk = 0; kk < C::KEYS / 16; ++kk)
-          mma_ss(tmem + C::O_COL, desc_from_lo(pa + ((kk * 32) >> 4)),
-                 desc_from_lo(vb + ((kk * 16 * 128) >> 4)), idesc, (jj > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(bars + 8 * C::B_P_FREE);
+          mma_ts(tmem + C::O_COL, tmem + C::KEYS * buf + 8 * kk, desc_from_lo(vb + ((kk * 16 * 128) >> 4)),
+                 idesc, (jj > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bars + 8 * (C::B_S_FREE + buf));
         tc_commit(bars + 8 * (C::B_EMPTY + slot));
         if (jj + 1 == n) tc_commit(bars + 8 * C::B_O_FINAL);
       }

@@ -7,7 +7,7 @@ schedule, key blocks and ring positions computed the same way.  Barriers have
 the hardware's parity semantics; loads and products complete after random
 delays, products of one thread in order.  A run reports deadlock, any wait a
 parity test could misread, and data hazards: a ring slot, the Q buffer, an S
-buffer, the P buffer or O read while it does not hold the reader's block (tile),
+buffer, the P packed over it or O read while it does not hold the reader's block (tile),
 or overwritten before its last reader."""
 import random
 
@@ -35,16 +35,16 @@ def blocks_of(p, t):
 
 
 class Sim:
-    def __init__(s, p, G, cta, seed, early_v=False, skip_sfree=False, skip_pfree=False):
+    def __init__(s, p, G, cta, seed, early_v=False, skip_sfree=False, one_pfull=False):
         # broken protocols for the model's own tests: early_v: V's slot released
-        # with P's arrival; skip_sfree: S written without its buffer read;
-        # skip_pfree: P written while P V may read it
+        # with P's arrival; skip_sfree: S written while P V may read the P over it;
+        # one_pfull: one P barrier for both buffers
         s.p, s.G, s.cta, s.rng = p, G, cta, random.Random(seed)
-        s.early_v, s.skip_sfree, s.skip_pfree = early_v, skip_sfree, skip_pfree
-        names = ['QF', 'QE', 'PFREE', 'OF'] + [f'{k}{i}' for i in range(p.ring) for k in ('K', 'V', 'E')] + \
-            ['SF0', 'SF1']
+        s.early_v, s.skip_sfree, s.one_pfull = early_v, skip_sfree, one_pfull
+        names = ['QF', 'QE', 'OF'] + [f'{k}{i}' for i in range(p.ring) for k in ('K', 'V', 'E')] + \
+            ['SF0', 'SF1', 'SFR0', 'SFR1']
         s.b = {n: Bar(n, 1) for n in names}
-        for n in ('SFR0', 'SFR1', 'PF'): s.b[n] = Bar(n, 4)
+        for n in ('PF0', 'PF1'): s.b[n] = Bar(n, 4)
         s.events, s.now, s.errors = [], 0, []
         s.mem, s.busy = {}, {}   # buffer -> tag; buffer -> end of its last reader
         s.pipe = {}              # MMA thread -> end of its last product
@@ -115,7 +115,8 @@ class Sim:
                 if blocks > 1 and not s.skip_sfree: yield from s.wait(f'SFR{buf}', (blocks >> 1) - 1, 'S')
                 end = s.product('S')
                 s.read(('ring', slot), (t, 'K', j), end); s.read('Q', t, end)
-                s.at(end, lambda buf=buf, tag=(t, j): s.write(('S', buf), tag))
+                for w in range(4): s.write((buf, w), None)  # its columns change from now on
+                s.at(end, lambda buf=buf, tag=('S', t, j): [s.write((buf, w), tag) for w in range(4)])
                 s.commit('S', f'SF{buf}'); s.commit('S', f'E{slot}')
                 if jj + 1 == len(bl): s.commit('S', 'QE')
                 blocks += 1
@@ -131,13 +132,14 @@ class Sim:
                 slot = (used + ring_v(jj, len(bl))) % p.ring
                 yield from s.wait(f'V{slot}', vu[slot], 'PV'); vu[slot] += 1
                 if s.early_v: s.b[f'E{slot}'].arrive()
-                yield from s.wait('PF', blocks, 'PV')
+                buf = blocks & 1
+                yield from (s.wait('PF0', blocks, 'PV') if s.one_pfull else s.wait(f'PF{buf}', blocks >> 1, 'PV'))
                 if jj == 0: s.write('O', None)
                 end = s.product('PV')
                 s.read(('ring', slot), (t, 'V', j), end)
-                for w in range(4): s.read(('P', w), (t, j), end)
+                for w in range(4): s.read((buf, w), ('P', t, j), end)
                 s.at(end, lambda tag=(t, j): s.write('O', tag))
-                s.commit('PV', 'PFREE')
+                s.commit('PV', f'SFR{buf}')
                 if not s.early_v: s.commit('PV', f'E{slot}')
                 if jj + 1 == len(bl): s.commit('PV', 'OF')
                 blocks += 1
@@ -155,14 +157,14 @@ class Sim:
                 buf = blocks & 1
                 yield from s.wait(f'SF{buf}', blocks >> 1, f'w{w}')
                 yield from pause()
-                s.read(('S', buf), (t, j), s.now)
-                s.b[f'SFR{buf}'].arrive()
+                s.read((buf, w), ('S', t, j), s.now)
                 yield from pause()
-                if blocks > 0 and not s.skip_pfree: yield from s.wait('PFREE', blocks - 1, f'w{w}')
-                if jj > 0 and s.rng.random() < 0.3: s.read('O', (t, bl[jj - 1]), s.now)  # rescale
-                s.write(('P', w), (t, j))
+                if jj > 0 and s.rng.random() < 0.3:  # rescale
+                    yield from s.wait(f'SFR{buf ^ 1}', (blocks - 1) >> 1, f'w{w}')
+                    s.read('O', (t, bl[jj - 1]), s.now)
+                s.write((buf, w), ('P', t, j))
                 yield from pause()
-                s.b['PF'].arrive()
+                s.b['PF0' if s.one_pfull else f'PF{buf}'].arrive()
                 blocks += 1
             yield from s.wait('OF', fin, f'w{w}'); fin += 1
             yield from pause()

@@ -22,7 +22,7 @@ def test_protocol_runs_clean(N, window, sinks, ring):
             assert not sim.errors, (cta, seed, sim.errors[:3])
 
 
-@pytest.mark.parametrize("flaw", ["early_v", "skip_sfree", "skip_pfree"])
+@pytest.mark.parametrize("flaw", ["early_v", "skip_sfree", "one_pfull"])
 def test_model_catches_a_broken_protocol(flaw):
     p = fm.P(1500, 300, 4)
     bad = 0
