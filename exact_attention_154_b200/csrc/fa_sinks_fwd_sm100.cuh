@@ -29,15 +29,16 @@
 // Blocks outside every row's view are neither loaded nor multiplied: a tile's
 // blocks are those holding sinks, then the window's.  Every wait is bounded.
 //
-// Measured (bf16, d = 128, 16 query heads on 2): window 256, 4 x 4096 rows,
-// 72 us; window 1024, 162 us; window 4096, 16384 rows, 560 us; 2 x 12 heads of
-// 333 rows at d = 64, 8.1 us.  The plain forward's shape given the same masks
-// (128-key blocks, two tiles and four softmax warpgroups a CTA, one CTA an SM)
-// took 111, 178, 519 and 12.2 us.  A block costs a warp about 2300 cycles with
-// both CTAs at work: 800 to 1000 the exponentials (64 a row, 16 a cycle and SM),
-// 150 to 400 reading S, the rest handing over (waits that have long been
-// fulfilled, the P stores and their fence); a tile about 2000 more at its end.
-// A part of the exponentials as a polynomial on the FMA pipe was 3% slower.
+// Measured (bf16, d = 128, 16 query heads on 2; inputs not in L2): window 256, 4 x
+// 4096 rows, 75 us; window 4096, 16384 rows, 519 us (928 TFLOP/s of visible pairs);
+// 2 x 12 heads of 333 rows at d = 64, 8.2 us.  The plain forward's shape given the
+// same masks (128-key blocks, two tiles and four softmax warpgroups a CTA, one CTA
+// an SM, P in shared memory) took 111, 519 and 12.2 us.  Under the wide window the
+// two CTAs of an SM take 1860 cycles a block each; the tensor pipe is busy 72% of
+// them (54% of its rate: a product with 64 keys on its wide side reads its 128
+// query rows for half as many columns), the exponential unit 53%.  A part of the
+// exponentials as a polynomial on the FMA pipe, and P handed over in halves, were no
+// faster under window 256 and 3% slower under the wide one.
 #pragma once
 
 #include "fa_fwd_sm100.cuh"
@@ -63,6 +64,15 @@ struct FastDiv {
 // The low n of 32 bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ float row_max32(const float* sv) {
+  float t[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i) t[i] = max3(sv[3 * i], sv[3 * i + 1], sv[3 * i + 2]);
+  t[10] = fmaxf(sv[30], sv[31]);
+  return max3(max3(t[0], t[1], t[2]), max3(t[3], t[4], t[5]),
+              max3(max3(t[6], t[7], t[8]), t[9], t[10]));
 }
 
 struct SinksFwdParams {
@@ -162,17 +172,17 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
     float m_ref = -INFINITY, l = 0.f;
     for (int jj = 0; jj < w.n; ++jj, ++blocks) {
       const int k0 = sinks_block(w, jj) * C::KEYS;
-      // Which keys the warp's 32 rows see, of the block and of each half of it:
-      // bounds that are the same for the whole warp (keys past the sequence's
-      // end lie past every row's own position).  Only a block that some row
-      // sees in part is masked, by bits; exponentials of a half that no row
-      // sees are not taken.
-      const bool all = k0 + C::KEYS - 1 <= row0 && (p.window < 0 || k0 >= row0 + 31 - p.window ||
-                                                    k0 + C::KEYS <= p.sinks);
-      bool none[2];
+      // Which keys the warp's 32 rows see, of each half of the block: bounds that
+      // are the same for the whole warp (keys past the sequence's end lie past
+      // every row's own position).  Only a half that some row sees in part is
+      // masked, by bits; one that no row sees is not looked at (by halves rather
+      // than whole blocks: window 256 2.5% faster).
+      bool all[2], none[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int ka = k0 + 32 * c;
+        all[c] = ka + 31 <= row0 &&
+                 (p.window < 0 || ka >= row0 + 31 - p.window || ka + 32 <= p.sinks);
         none[c] = ka > row0 + 31 || (p.window >= 0 && ka + 31 < row0 - p.window && ka >= p.sinks);
       }
       const int buf = blocks & 1;
@@ -186,22 +196,28 @@ __device__ void sinks_softmax(const SinksFwdParams& p, uint32_t base, uint32_t t
       float sv[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(sr[c]);
-      if (!all) {
-        uint32_t bits[2];
+      float m_blk = -INFINITY;
+      if (all[0] && all[1]) {
+        m_blk = row_max64(sv);
+      } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int rel = row - k0 - 32 * c;
-          bits[c] = low_bits(rel + 1);
-          if (p.window >= 0)
-            bits[c] &= ~low_bits(rel - p.window) | low_bits(p.sinks - k0 - 32 * c);
-        }
+          if (none[c]) continue;
+          if (!all[c]) {
+            const int rel = row - k0 - 32 * c;
+            uint32_t bits = low_bits(rel + 1);
+            if (p.window >= 0) bits &= ~low_bits(rel - p.window) | low_bits(p.sinks - k0 - 32 * c);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) sv[c] = (bits[c / 32] >> (c % 32)) & 1u ? sv[c] : -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              sv[32 * c + i] = (bits >> i) & 1u ? sv[32 * c + i] : -INFINITY;
+          }
+          m_blk = fmaxf(m_blk, row_max32(sv + 32 * c));
+        }
       }
+      m_blk *= sl2;
       // Lazy reference, as in the plain forward: moved only when the block's
       // maximum exceeds it by more than 2^8, and by the first block.  A row
       // that has seen no key yet has m_ref = -inf, l = 0 and O = 0.
-      const float m_blk = row_max64(sv) * sl2;
       const bool rescale = jj > 0 && m_blk > m_ref + kLazyRescaleLog2;
       const float m_new = jj == 0 || rescale ? m_blk : m_ref;
       const float alpha = jj == 0 || m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
