@@ -9,7 +9,7 @@
 //
 // What bounds it under a window: latency.  A 128-row query tile meets only
 // window / 64 + 3 blocks of 64 keys, so the chain of a block (scores,
-// exponentials, weights to shared memory) and what a tile starts and ends with
+// exponentials, weights back to TMEM) and what a tile starts and ends with
 // are not hidden behind other blocks of the same tile.  So tiles are kept
 // small and independent, and two CTAs share an SM (d <= 128): one computes
 // while the other starts, ends or waits.  One warpgroup owns a tile's rows
@@ -30,7 +30,7 @@
 // blocks are those holding sinks, then the window's.  Every wait is bounded.
 //
 // Measured (bf16, d = 128, 16 query heads on 2; inputs not in L2): window 256, 4 x
-// 4096 rows, 75 us; window 4096, 16384 rows, 519 us (928 TFLOP/s of visible pairs);
+// 4096 rows, 76 us; window 4096, 16384 rows, 519 us (928 TFLOP/s of visible pairs);
 // 2 x 12 heads of 333 rows at d = 64, 8.2 us.  The plain forward's shape given the
 // same masks (128-key blocks, two tiles and four softmax warpgroups a CTA, one CTA
 // an SM, P in shared memory) took 111, 519 and 12.2 us.  Under the wide window the

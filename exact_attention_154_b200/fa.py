@@ -382,7 +382,8 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
     ``j <= i and (i - j <= window or j < sinks)`` (``window=-1``: plain causal).
 
     ``q`` is ``[B, H, N, d]``, ``k`` and ``v`` ``[B, Hk, N, d]`` (each key head
-    shared by ``H / Hk`` query heads), of any strides with adjacent row elements.
+    shared by ``H / Hk`` query heads), of any strides that are multiples of 8 with
+    adjacent row elements (an expanded dimension, stride 0, is refused).
     Returns ``(O [B, H, N, d], LSE [B, H, N])``, contiguous; LSE is None when
     ``return_lse`` is False."""
     return _done("fa_fwd_sinks", (_torch_calls or _calls()).fwd_sinks(
@@ -404,8 +405,8 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
                  window: int, sinks: int, scale: float | None = None,
                  out: torch.Tensor | None = None, return_lse: bool = True):
     """:func:`fwd_sinks` one token at a time: ``q`` ``[B, H, d]`` holds each
-    sequence's newest query, ``k`` and ``v`` ``[B, Hk, S, d]`` (any strides with
-    adjacent row elements) its cached keys and values, of which the first
+    sequence's newest query, ``k`` and ``v`` ``[B, Hk, S, d]`` (strides as
+    there) its cached keys and values, of which the first
     ``seqlens[b]`` (int32 ``[B]``, the newest token included) are in use.
     Returns ``(O [B, H, d], LSE [B, H])``; a length of 0 gives O = 0 and LSE =
     -inf.  Cache rows that are not visible may hold anything."""
@@ -446,8 +447,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch
                  k_out: torch.Tensor | None = None):
     """RMS norm of every head's query and key and the rotation by position.
 
-    ``q`` is ``[B, H, N, d]``, ``k`` ``[B, Hk, N, d]``, of any strides with
-    adjacent row elements (views of a packed projection, ``transpose(1, 2)`` of
+    ``q`` is ``[B, H, N, d]``, ``k`` ``[B, Hk, N, d]``, of any strides that
+    are multiples of 8 with adjacent row elements (views of a packed projection, ``transpose(1, 2)`` of
     ``[B, N, H, d]``).  ``cos``, ``sin``: ``[max_pos, rot / 2]`` fp32
     (:func:`rope_table`); ``positions`` int32 ``[B, N]`` (None: the row index).
     ``q_weight``, ``k_weight``: ``[d]``, or None to leave that operand

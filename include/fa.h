@@ -253,7 +253,7 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
  *                head h reads key / value head h / (H / Hk)
  *   *_strides  : host pointers to {batch, head, row} strides in elements, or
  *                NULL for a contiguous tensor, as in fa_qk_norm_rope
- *   o          : [B, H, N, d] contiguous (written)
+ *   o          : [B, H, N, d] contiguous (written); overlaps no input
  *   lse        : [B, H, N] fp32 (written), or NULL
  *   window     : >= 0, or -1: every earlier key is visible (plain causal)
  *   sinks      : >= 0 (0: the window alone)
@@ -277,7 +277,8 @@ int fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *ls
  *                as fa_fwd_sinks left them for the same arguments
  *   dq         : [B, H, N, d] contiguous (written)
  *   dk, dv     : [B, Hk, N, d] contiguous (written): summed over the query heads
- *                that share the key / value head, in a fixed order
+ *                that share the key / value head, in a fixed order.  No output
+ *                overlaps an input.
  *   workspace  : fa_bwd_sinks_workspace(...) fp32, caller-owned scratch,
  *                32-byte aligned
  *   d          : 64 or 128
