@@ -117,7 +117,8 @@ __device__ __forceinline__ float row_dot(const float2 (&x)[8], const float2 (&y)
 }
 
 // Threads, and CTAs of an SM that the registers are limited for (80 and 128).
-// Measured on 16384 tokens x 18 heads of 128, forward / gradient: 32.4 / 53 us;
+// Measured on 16384 tokens x 18 heads of 128, forward / gradient, before rows were
+// requested ahead (with it, inputs not in L2: 28.8 / 53.7): 32.4 / 53 us;
 // 64 registers (spilled) 41 / 83, 128 in the forward 37; d / 8 lanes a row with
 // 8-byte pieces 35 / 70 (its per-row instructions weigh twice as much), and the
 // same with rows through a ring of asynchronous copies 42 / 59.
@@ -183,8 +184,17 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
         g_at += gh;
       }
     };
+    // the row `by` heads after x_at's to L2: the registers hold one row on its way,
+    // too little to cover the latency of memory (forward 33.0 -> 28.8 us; the
+    // gradient, with two operands' rows, lost 4%)
+    auto ahead = [&](int by) {
+      if (!BWD) asm volatile("prefetch.global.L2 [%0];" ::"l"(x_at + by * xh + 16 * sub));
+    };
     uint4 xv[2], gv[2];
     load(xv, gv);  // before the position, which the cos / sin loads wait for
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (i < heads) ahead(i - 1);
     int pos = n;
     if (p.positions != nullptr) pos = __ldg(p.positions + token);
     if (pos < 0 || pos >= p.max_pos) {
@@ -232,6 +242,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
       }
       if constexpr (!BWD) {
         if (h + 1 < heads) load(xv, gv);
+        if (h + 4 < heads) ahead(2);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(partner<INTER>(x, k), other_c[k]));
