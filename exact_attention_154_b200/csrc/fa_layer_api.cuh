@@ -87,9 +87,22 @@ int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   qk_norm_rope_kernel<HD, BF16, INTER, BWD><<<grid, kRopeThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (BWD && (p.op[0].w != nullptr || p.op[1].w != nullptr)) {
-    norm_weight_sum_kernel<BF16><<<dim3(d / 32, 2), 1024, 0, stream>>>(
-        p.parts, p.ctas_q, grid, d, p.op[0].dw, p.op[1].dw, p.w_fp32);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(d / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    std::memset(&attr, 0, sizeof(attr));
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, norm_weight_sum_kernel<BF16>, static_cast<const float*>(p.parts),
+                           p.ctas_q, grid, d, p.op[0].dw, p.op[1].dw, p.w_fp32) != cudaSuccess) {
+      cudaGetLastError();
+      return FA_ERR_CUDA;
+    }
   }
   return FA_OK;
 }

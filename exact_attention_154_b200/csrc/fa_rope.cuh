@@ -153,6 +153,9 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
   const long long xh = op.xh, gh = op.gh, yh = op.yh;
   float2 w[8], dw[8];
   if constexpr (BWD) {
+    // norm_weight_sum_kernel may take its place, and waits there for this grid's end
+    // (gradient 55.3 -> 53.7 us, a small one 19.1 -> 18.4)
+    asm volatile("griddepcontrol.launch_dependents;");
     load_weight8<BF16>(op.w, p.w_fp32, ea, w);
     load_weight8<BF16>(op.w, p.w_fp32, eb, w + 4);
   }
@@ -322,10 +325,11 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
 // fixed order (32 columns a block, 32 warps over the parts, then the warps in
 // order), rounded to the weight's type.
 template <bool BF16>
-__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* __restrict__ parts,
-                                                               int ctas_q, int ctas, int d, void* dq,
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* parts, int ctas_q,
+                                                               int ctas, int d, void* dq,
                                                                void* dk, int w_fp32) {
   __shared__ float sums[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // `parts` is written now
   void* out = blockIdx.y == 0 ? dq : dk;
   if (out == nullptr) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
