@@ -31,9 +31,9 @@
 // need.  The dQ kernel has no P to keep, so its S(it+1) only waits for S(it) to
 // be read, and two dP regions let dP(it+1) precede dS(it).
 //
-// Measured (bf16, d = 128): window 256, 4 x 4096 rows, 16 query heads on 2, 255
-// us (dK/dV 161, dQ beside it and after, row statistic 23, sums 7); window 2048,
-// 8205 rows, 16 heads on 4, 445 us.  A dK/dV step takes about 3400 cycles, of
+// Measured (bf16, d = 128; inputs not in L2): window 256, 4 x 4096 rows, 16 query
+// heads on 2, 281 us (alone dK/dV 158, dQ 131, beside it and after; row statistic
+// 23, sums 7); window 2048, 8205 rows, 16 heads on 4, 465 us.  A dK/dV step takes about 3400 cycles, of
 // which its four products need 2048.  Masks found from the warp's bounds and one
 // vote a step gained 2% over votes on the bits and at each wait.
 //
