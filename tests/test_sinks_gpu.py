@@ -200,6 +200,29 @@ def test_large_scores():
     assert np.abs(layer.f64(lse) - L).max() <= 2.0 ** -9
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_reference_that_moves_in_every_block(d):
+    # keys grow along the sequence, so a row's maximum keeps rising: O is rescaled
+    # block after block, over several tiles of a CTA (d = 256: one CTA an SM)
+    B, H, N = 2, 20, 1100
+    q, k, v = qkv(B, H, 1, N, d, torch.bfloat16, 545 + d)
+    q = q.abs()
+    k = (k.abs() * (0.2 + torch.arange(N, device="cuda") / 400)[:, None]).to(torch.bfloat16)
+    for window in (-1, 300):
+        o, lse = fa.fwd_sinks(q, k, v, window, 4)
+        torch.cuda.synchronize()
+        p, L = layer.sinks_probs(q, k, window, 4, fa.default_scale(d))
+        vd = np.repeat(layer.f64(v), H, axis=1)
+        # scores: all terms positive, so a sum of moduli is the score itself; each
+        # of its d additions and the scaling round by 2^-24 of at most its value
+        top = (layer.f64(q).max() * layer.f64(k).max() * d * fa.default_scale(d))
+        rel = 2.0 ** -24 * (d + 4) * top
+        u = 2.0 ** -8
+        allowed = (u + 2 * rel + 2.0 ** -12) * (p @ np.abs(vd)) + u * np.abs(p @ vd)
+        assert (np.abs(layer.f64(o) - p @ vd) <= allowed).all()
+        assert np.abs(layer.f64(lse) - L).max() <= rel + 2.0 ** -12 + 2.0 ** -23 * np.abs(L).max()
+
+
 def test_graph_replay_and_two_streams():
     q, k, v = qkv(1, 4, 2, 700, 64, torch.bfloat16, 550)
     dout = torch.randn_like(q)
