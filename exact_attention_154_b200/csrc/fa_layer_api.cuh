@@ -54,7 +54,7 @@ struct RopeArgs {
   float eps;
 };
 
-template <int HD, bool BF16, bool INTER, bool BWD>
+template <int HD, bool BF16, bool INTER, bool PART, bool BWD>
 int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   constexpr int kTokens = 32 / (HD / 16), kWarps = kRopeThreads / 32;
   const int HT = p.op[0].heads + p.op[1].heads;
@@ -84,7 +84,7 @@ int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   }
   p.ctas_q = (int)ctas[0];
   const int grid = (int)(ctas[0] + ctas[1]);
-  qk_norm_rope_kernel<HD, BF16, INTER, BWD><<<grid, kRopeThreads, 0, stream>>>(p);
+  qk_norm_rope_kernel<HD, BF16, INTER, PART, BWD><<<grid, kRopeThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (BWD && (p.op[0].w != nullptr || p.op[1].w != nullptr)) {
     cudaLaunchConfig_t cfg;
@@ -107,13 +107,19 @@ int launch_rope(RopeParams& p, DeviceState& st, int d, cudaStream_t stream) {
   return FA_OK;
 }
 
+template <int HD, bool BF16, bool BWD>
+int launch_rope_form(RopeParams& p, DeviceState& st, const RopeArgs& a, cudaStream_t stream) {
+  if (a.rot == HD)
+    return a.interleaved ? launch_rope<HD, BF16, true, false, BWD>(p, st, a.d, stream)
+                         : launch_rope<HD, BF16, false, false, BWD>(p, st, a.d, stream);
+  return a.interleaved ? launch_rope<HD, BF16, true, true, BWD>(p, st, a.d, stream)
+                       : launch_rope<HD, BF16, false, true, BWD>(p, st, a.d, stream);
+}
+
 template <int HD, bool BWD>
 int launch_rope_types(RopeParams& p, DeviceState& st, const RopeArgs& a, cudaStream_t stream) {
-  if (a.dtype == FA_BF16)
-    return a.interleaved ? launch_rope<HD, true, true, BWD>(p, st, a.d, stream)
-                         : launch_rope<HD, true, false, BWD>(p, st, a.d, stream);
-  return a.interleaved ? launch_rope<HD, false, true, BWD>(p, st, a.d, stream)
-                       : launch_rope<HD, false, false, BWD>(p, st, a.d, stream);
+  return a.dtype == FA_BF16 ? launch_rope_form<HD, true, BWD>(p, st, a, stream)
+                            : launch_rope_form<HD, false, BWD>(p, st, a, stream);
 }
 
 template <bool BWD>

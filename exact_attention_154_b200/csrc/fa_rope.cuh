@@ -125,11 +125,16 @@ __device__ __forceinline__ float row_dot(const float2 (&x)[8], const float2 (&y)
 constexpr int kRopeThreads = 128;
 constexpr int kRopeFwdCtas = 6, kRopeBwdCtas = 4;
 
+// PART: rot < HD, and some lanes' columns stay as they are: selects keep them apart from
+// their neighbours.  With rot == HD there are none, and the selects fall away (16384
+// tokens x 18 heads, forward / gradient: 64 of 128 columns 27.8 / 53.7 us, 128 of 128
+// 26.6 / 52.2; a branch on the lane, in every call, 28.7 / 54.8 for 128 of 128).
+//
 // A CTA's item: up to heads_per_warp heads of q or k x one group of 32 / (HD / 16)
 // tokens for each warp.  Lanes without a token compute its last one again and
 // write nothing.  BWD: turns the arriving gradient back and takes it through
 // the norm; each CTA sums its rows' g * n and leaves the sums in `parts`.
-template <int HD, bool BF16, bool INTER, bool BWD>
+template <int HD, bool BF16, bool INTER, bool PART, bool BWD>
 __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCtas)
     qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = HD / 16;        // lanes of a row
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
   const int sub = lane % LANES;
   const int half = p.rot / 2;
   // this lane's columns: ea .. ea + 7 and eb .. eb + 7
-  const bool turned = 16 * sub < p.rot;
+  const bool turned = !PART || 16 * sub < p.rot;
   const int ea = !INTER && turned ? 8 * sub : 16 * sub;
   const int eb = !INTER && turned ? half + 8 * sub : 16 * sub + 8;
   const bool is_k = static_cast<int>(blockIdx.x) >= p.ctas_q;
@@ -206,9 +211,12 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
       live = false;
       pos = 0;
     }
-    float2 c[4], sn[4];  // of the lane's eight pairs
+    // Of the lane's eight pairs.  Columns past rot are their own times 1 plus a zero in
+    // place of their neighbour times -0: the neighbour may be infinite, and adding
+    // -0 changes nothing, not even the sign of a zero.
+    float2 c[4], sn[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = make_float2(1.f, 1.f), sn[k] = make_float2(0.f, 0.f);
+    for (int k = 0; k < 4; ++k) c[k] = make_float2(1.f, 1.f), sn[k] = make_float2(-0.f, -0.f);
     if (turned) {
       const long long at = static_cast<long long>(pos) * half + 8 * sub;
       load_float8(p.cos + at, c);
@@ -234,6 +242,7 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
         }
         own_c[k] = __fmul2_rn(own_c[k], w[k]);
         other_c[k] = __fmul2_rn(other_c[k], partner<INTER>(w, k));
+        if (!turned) other_c[k] = make_float2(-0.f, -0.f);
       }
     }
 #pragma unroll 1
@@ -247,8 +256,10 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
         if (h + 1 < heads) load(xv, gv);
         if (h + 4 < heads) ahead(2);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(partner<INTER>(x, k), other_c[k]));
+        for (int k = 0; k < 8; ++k) {
+          const float2 z = partner<INTER>(x, k);
+          o[k] = __ffma2_rn(x[k], own_c[k], __fmul2_rn(turned ? z : make_float2(0.f, 0.f), other_c[k]));
+        }
         if (normed) {
           const float r = rsqrtf(row_dot<LANES>(x, x) * (1.f / HD) + p.eps);
           const float2 rr = make_float2(r, r);
@@ -266,14 +277,17 @@ __global__ void __launch_bounds__(kRopeThreads, BWD ? kRopeBwdCtas : kRopeFwdCta
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float ck = k & 1 ? c[k / 2].y : c[k / 2].x, sk = k & 1 ? sn[k / 2].y : sn[k / 2].x;
-              o[k] = make_float2(y[k].x * ck + y[k].y * sk, y[k].y * ck - y[k].x * sk);
+              const float a = turned ? y[k].x : -0.f, b = turned ? y[k].y : 0.f;
+              o[k] = make_float2(y[k].x * ck + b * sk, y[k].y * ck - a * sk);
             }
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              o[k] = __ffma2_rn(y[k], c[k], __fmul2_rn(y[k + 4], sn[k]));
-              o[k + 4] = make_float2(y[k + 4].x * c[k].x - y[k].x * sn[k].x,
-                                     y[k + 4].y * c[k].y - y[k].y * sn[k].y);
+              const float2 a = turned ? y[k] : make_float2(-0.f, -0.f);
+              const float2 b = turned ? y[k + 4] : make_float2(0.f, 0.f);
+              o[k] = __ffma2_rn(y[k], c[k], __fmul2_rn(b, sn[k]));
+              o[k + 4] = make_float2(y[k + 4].x * c[k].x - a.x * sn[k].x,
+                                     y[k + 4].y * c[k].y - a.y * sn[k].y);
             }
           }
         }
