@@ -353,11 +353,14 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) decode_kernel(const __grid_
             }
         }
       }
+      // (a warp that has met only scores of -infinity has no reference yet, and its
+      // weights are 0: finite queries and keys reach that where fp32 overflows)
+      const float ref[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
       for (int j = 0; j < C::TILES; ++j) {
         float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(s[j][n][i] - m[n][i & 1]);
+        for (int i = 0; i < 4; ++i) e[i] = ex2(s[j][n][i] - ref[i & 1]);
         l[n][0] += e[0] + e[2];
         l[n][1] += e[1] + e[3];
         // weights in 16 bits, as the matrix instruction takes them beside V
