@@ -429,6 +429,8 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str = "no
         raise ValueError("device must be a CUDA device")
     if max_pos < 1 or rot < 2:
         raise ValueError("max_pos and rot must be positive")
+    if max(max_pos, rot) > 2 ** 31 - 1 or not -2 ** 31 <= original_max_pos < 2 ** 31:
+        raise ValueError("max_pos, rot and original_max_pos must fit 32 bits")
     cos = torch.empty((max_pos, rot // 2), device=dev, dtype=torch.float32)
     sin = torch.empty_like(cos)
     with _on(cos.device):
