@@ -11,6 +11,7 @@
 #include <dlfcn.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -88,6 +89,20 @@ at::Tensor new_like(const at::Tensor& t) { return at::empty(t.sizes(), t.options
 int as_int(int64_t n) {
   if (n < INT32_MIN || n > INT32_MAX) refuse("a size does not fit 32 bits");
   return static_cast<int>(n);
+}
+
+// Refuses an output that lies over `in`: other blocks of the grid may still read there.
+// The same elements in the same places are taken where a block reads all of its rows
+// before it writes them (same_ok).  Only what is certain is refused: interleaved views,
+// as of one packed projection, may be apart though their ranges meet.
+void keep_apart(const at::Tensor& out, const char* name, const at::Tensor& in, const char* in_name,
+                bool same_ok) {
+  const bool at_start = out.data_ptr() == in.data_ptr();
+  const bool same = at_start && out.sizes() == in.sizes() && out.strides() == in.strides();
+  const auto overlap = at::get_overlap_status(out, in);
+  if (same ? !same_ok
+           : at_start || overlap == at::MemOverlapStatus::Partial || overlap == at::MemOverlapStatus::Full)
+    refuse(std::string(name) + " overlaps " + in_name);
 }
 
 // `like`'s shape and type, contiguous, on its device.
@@ -236,6 +251,15 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
   const Table t = table(a[2], a[3], a[4], q);
   const Weights w = weights(a[5], a[6], q);
   const at::Tensor qo = output(a[9], "q_out", q), ko = output(a[10], "k_out", k);
+  if (a[9] != Py_None) {
+    keep_apart(qo, "q_out", q, "q", true);
+    keep_apart(qo, "q_out", k, "k", false);
+  }
+  if (a[10] != Py_None) {
+    keep_apart(ko, "k_out", k, "k", true);
+    keep_apart(ko, "k_out", q, "q", false);
+  }
+  if (a[9] != Py_None && a[10] != Py_None) keep_apart(qo, "q_out", ko, "k_out", false);
   const OnDevice on(q);
   const int rc = p_norm_rope(
       data(q), data(k), data(qo), data(ko), strides(q), strides(k), strides(qo), strides(ko),
@@ -285,6 +309,12 @@ void check_kv(const at::Tensor& k, const at::Tensor& v, int64_t B, int64_t H, in
       k.size(1) < 1 || H % k.size(1) != 0)
     refuse("k and v must be [B, Hk, rows, d] with q's B and d (and N), H a multiple of Hk");
 }
+// An attention's given output against its inputs.
+void apart_from(const at::Tensor& o, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v) {
+  keep_apart(o, "out", q, "q", true);
+  keep_apart(o, "out", k, "k", false);
+  keep_apart(o, "out", v, "v", false);
+}
 float scale_of(PyObject* o) { return o == Py_None ? 0.f : static_cast<float>(number(o)); }
 
 // (q, k, v, window, sinks, scale, out, lse, return_lse)
@@ -296,6 +326,7 @@ PyObject* fwd_sinks(PyObject* const* a, Py_ssize_t n) {
   check_kv(k, v, q.size(0), q.size(1), q.size(2), q.size(3));
   const int window = whole(a[3]), sinks = whole(a[4]);
   const at::Tensor o = a[6] == Py_None ? new_like(q) : contiguous_like(a[6], "out", q);
+  if (a[6] != Py_None) apart_from(o, q, k, v);
   const int with_lse = truth(a[8]);
   at::Tensor lse;
   if (with_lse)
@@ -356,6 +387,7 @@ PyObject* decode_sinks(PyObject* const* a, Py_ssize_t n) {
   same_device(lens, "seqlens", q);
   const int window = whole(a[4]), sinks = whole(a[5]);
   const at::Tensor o = a[7] == Py_None ? new_like(q) : contiguous_like(a[7], "out", q);
+  if (a[7] != Py_None) apart_from(o, q, k, v);
   const int with_lse = truth(a[8]);
   at::Tensor lse;
   if (with_lse) lse = at::empty(q.sizes().slice(0, 2), q.options().dtype(at::kFloat));

@@ -385,7 +385,9 @@ def fwd_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, si
     shared by ``H / Hk`` query heads), of any strides that are multiples of 8 with
     adjacent row elements (an expanded dimension, stride 0, is refused).
     Returns ``(O [B, H, N, d], LSE [B, H, N])``, contiguous; LSE is None when
-    ``return_lse`` is False."""
+    ``return_lse`` is False.  ``out`` lies over none of the inputs, but may be ``q``.
+    All rows hold finite values, those of padding too: a masked weight is 0, and 0 times
+    an infinity or NaN is not."""
     return _done("fa_fwd_sinks", (_torch_calls or _calls()).fwd_sinks(
         q, k, v, window, sinks, scale, out, lse, return_lse))
 
@@ -409,7 +411,7 @@ def decode_sinks(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seqlens: tor
     there) its cached keys and values, of which the first
     ``seqlens[b]`` (int32 ``[B]``, the newest token included) are in use.
     Returns ``(O [B, H, d], LSE [B, H])``; a length of 0 gives O = 0 and LSE =
-    -inf.  Cache rows that are not visible may hold anything."""
+    -inf.  Cache rows that are not visible may hold anything.  ``out`` may be ``q``."""
     return _done("fa_decode_sinks", (_torch_calls or _calls()).decode_sinks(
         q, k, v, seqlens, window, sinks, scale, out, return_lse))
 
@@ -455,7 +457,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos: torch.Tensor, sin: torch
     (:func:`rope_table`); ``positions`` int32 ``[B, N]`` (None: the row index).
     ``q_weight``, ``k_weight``: ``[d]``, or None to leave that operand
     unnormalised.  Returns ``(q_out, k_out)``, contiguous unless given; they
-    may be ``q`` and ``k`` themselves."""
+    may be ``q`` and ``k`` themselves, and share no other memory with them or each other."""
     return _done("fa_qk_norm_rope", (_torch_calls or _calls()).qk_norm_rope(
         q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out))
 

@@ -253,7 +253,8 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
  *                head h reads key / value head h / (H / Hk)
  *   *_strides  : host pointers to {batch, head, row} strides in elements, or
  *                NULL for a contiguous tensor, as in fa_qk_norm_rope
- *   o          : [B, H, N, d] contiguous (written); overlaps no input
+ *   o          : [B, H, N, d] contiguous (written); may be q itself where q is
+ *                contiguous, and overlaps no other input
  *   lse        : [B, H, N] fp32 (written), or NULL
  *   window     : >= 0, or -1: every earlier key is visible (plain causal)
  *   sinks      : >= 0 (0: the window alone)
@@ -296,7 +297,8 @@ int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, con
  * token's own among them).  With n = seqlens[b], row j of the cache is visible
  * iff j < n and (j >= n - 1 - window or j < sinks).
  *
- *   q, o       : [B, H, d] contiguous;  lse : [B, H] fp32, or NULL
+ *   q, o       : [B, H, d] contiguous (o may be q itself, and overlaps neither k nor
+ *                v);  lse : [B, H] fp32, or NULL
  *   k, v       : caches [B, Hk, S, d] of the given strides (as fa_fwd_sinks: also
  *                [B, S, Hk, d] by its strides), read only; rows that are not visible
  *                may hold anything
