@@ -46,11 +46,20 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library and its torch binding next to the package; returns
-    the library's path."""
-    build_binding(force)
-    if not force and up_to_date():
+    """Compile the library next to the package, then, where torch is installed, its
+    torch binding; returns the library's path.  (A program that calls the C ABI
+    needs no torch, nor a binding that compiles.)"""
+    if force or not up_to_date():
+        build_library(verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
         return LIB
+    build_binding(force)
+    return LIB
+
+
+def build_library(verbose: bool = False) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc_path(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
            "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
@@ -61,7 +70,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(res.stderr)
     check_register_split(res.stdout + res.stderr)
     os.replace(tmp, LIB)
-    return LIB
 
 
 def build_binding(force: bool = False) -> str:

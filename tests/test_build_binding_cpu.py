@@ -1,0 +1,55 @@
+"""The build of the library and of its torch side: the C library needs no torch."""
+import os
+import subprocess
+import sys
+import types
+
+import pytest
+
+from exact_attention_154_b200 import _build
+
+
+def test_the_library_builds_without_torch(tmp_path):
+    _build.build()  # (current, so the child below compiles nothing)
+    code = """
+import importlib.util, sys
+sys.modules["torch"] = None  # as if it were not installed
+spec = importlib.util.spec_from_file_location("b", sys.argv[1])
+b = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(b)
+b.BINDING = sys.argv[2]      # (none there yet)
+print(b.build() == b.LIB)
+"""
+    r = subprocess.run([sys.executable, "-c", code, _build.__file__, str(tmp_path / "none.so")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "True", r.stderr
+
+
+def compiles(monkeypatch):
+    """What the build compiles, by compiler, instead of compiling it."""
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(os.path.basename(cmd[0]))
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    monkeypatch.setattr(_build.os, "replace", lambda a, b: os.remove(a))
+    return ran
+
+
+def test_the_library_comes_first(monkeypatch, tmp_path):
+    # a binding that does not compile leaves the library built
+    ran = compiles(monkeypatch)
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(_build, "check_register_split", lambda log: None)
+
+    def fail(force=False):
+        ran.append("binding")
+        raise RuntimeError("g++ failed")
+
+    monkeypatch.setattr(_build, "build_binding", fail)
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
+        _build.build()
+    assert ran == ["nvcc", "binding"]
