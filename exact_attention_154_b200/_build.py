@@ -9,7 +9,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa_sm100.so")
-BINDING = os.path.join(PKG, "_fa_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
 SOURCES = ["fa_api.cu"]
 
@@ -72,13 +71,30 @@ def build_library(verbose: bool = False) -> None:
     os.replace(tmp, LIB)
 
 
+BINDING_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared"]
+
+
+def binding_path() -> str:
+    """The torch binding's file for the running torch and Python: its classes'
+    layout and its module's form are theirs, so each has a file of its own."""
+    import hashlib
+    import sysconfig
+
+    import torch
+    key = "\n".join([torch.__version__, str(torch.version.cuda),
+                     str(int(torch._C._GLIBCXX_USE_CXX11_ABI)),
+                     str(sysconfig.get_config_var("SOABI")), *BINDING_FLAGS])
+    return os.path.join(PKG, f"_fa_torch-{hashlib.sha256(key.encode()).hexdigest()[:12]}.so")
+
+
 def build_binding(force: bool = False) -> str:
     """Compile the torch side of the layer's calls (host code, resolved against
-    the library when it is loaded)."""
+    the library when it is loaded); returns its path."""
+    binding = binding_path()
     inputs = [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h")]
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
-        return BINDING
+    if not force and os.path.exists(binding) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(binding) for f in inputs):
+        return binding
     import sysconfig
 
     import torch
@@ -87,8 +103,8 @@ def build_binding(force: bool = False) -> str:
     include = [os.path.join(root, "include"),
                os.path.join(root, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+    tmp = binding + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", *BINDING_FLAGS,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for p in include for x in ("-isystem", p)], "-o", tmp, BINDING_SOURCE,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
@@ -96,8 +112,8 @@ def build_binding(force: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, binding)
+    return binding
 
 
 # The two-Q-tile kernels run 640 threads (96 registers each at launch) and

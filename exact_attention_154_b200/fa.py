@@ -10,12 +10,15 @@ sm_100 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
 
 import torch
 
+from . import _build
 from .synth import BF16, FP16
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa_sm100.so")
@@ -357,11 +360,18 @@ def _calls():
     global _torch_calls
     if _torch_calls is None:
         load()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path}, the torch binding, is missing for torch {torch.__version__} "
+                               "and this Python: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._fa_torch", path)
+        spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
         try:
-            from . import _fa_torch
+            _fa_torch = importlib.util.module_from_spec(spec)
+            loader.exec_module(_fa_torch)
         except ImportError as e:
-            raise RuntimeError("the torch binding is missing: build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+            raise RuntimeError(f"the torch binding does not load: {e}") from e
         _fa_torch.load(_LIB_PATH)
         _torch_calls = _fa_torch
     return _torch_calls

@@ -1,12 +1,14 @@
-"""The build of the library and of its torch side: the C library needs no torch."""
+"""The build of the library and of its torch side: the C library needs no torch, and the
+torch side is one for each torch and Python it is compiled against."""
 import os
 import subprocess
 import sys
 import types
 
 import pytest
+import torch
 
-from exact_attention_154_b200 import _build
+from exact_attention_154_b200 import _build, fa
 
 
 def test_the_library_builds_without_torch(tmp_path):
@@ -39,6 +41,21 @@ def compiles(monkeypatch):
     return ran
 
 
+@pytest.mark.parametrize("change", ["torch", "abi", "python", "nothing"])
+def test_the_binding_belongs_to_its_torch_and_python(monkeypatch, change):
+    _build.build()
+    ran = compiles(monkeypatch)
+    if change == "torch":
+        monkeypatch.setattr(torch, "__version__", "99.9.0")
+    if change == "abi":
+        monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    if change == "python":
+        import sysconfig
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other")
+    _build.build_binding()
+    assert ran == ([] if change == "nothing" else ["g++"])
+
+
 def test_the_library_comes_first(monkeypatch, tmp_path):
     # a binding that does not compile leaves the library built
     ran = compiles(monkeypatch)
@@ -53,3 +70,17 @@ def test_the_library_comes_first(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         _build.build()
     assert ran == ["nvcc", "binding"]
+
+
+def test_a_binding_that_is_not_there_or_does_not_load_is_named(monkeypatch, tmp_path):
+    _build.build()
+    path = str(tmp_path / "_fa_torch-0.so")
+    monkeypatch.setattr(fa, "_torch_calls", None)
+    monkeypatch.setattr(_build, "binding_path", lambda: path)
+    x = torch.zeros(1, 1, 8, 64, dtype=torch.float16)
+    with pytest.raises(RuntimeError, match="missing for torch"):
+        fa.fwd_sinks(x, x, x, 4, 1)
+    with open(path, "w") as f:
+        f.write("not a library")
+    with pytest.raises(RuntimeError, match="does not load: .*_fa_torch-0.so"):
+        fa.fwd_sinks(x, x, x, 4, 1)
