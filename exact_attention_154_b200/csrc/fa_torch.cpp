@@ -97,6 +97,7 @@ int as_int(int64_t n) {
 // as of one packed projection, may be apart though their ranges meet.
 void keep_apart(const at::Tensor& out, const char* name, const at::Tensor& in, const char* in_name,
                 bool same_ok) {
+  if (out.numel() == 0 || in.numel() == 0) return;  // (the library refuses those sizes)
   const bool at_start = out.data_ptr() == in.data_ptr();
   const bool same = at_start && out.sizes() == in.sizes() && out.strides() == in.strides();
   const auto overlap = at::get_overlap_status(out, in);

@@ -93,3 +93,14 @@ def test_attention_refuses_overlaps():
     for out in (k[:, 0, :2], v[:, 1, 5:7], k[:, 1, 128:130]):
         with pytest.raises(ValueError, match="out overlaps"):
             fa.decode_sinks(one, k, v, lens, 64, 4, out=out)
+
+
+def test_empty_operands_are_refused_for_their_size():
+    q, k = randn(0, 2, 8, 64), randn(0, 1, 8, 64)
+    with pytest.raises(fa.FaError):
+        fa.fwd_sinks(q, k, k, 4, 1, out=torch.empty_like(q))
+    with pytest.raises(fa.FaError):
+        fa.qk_norm_rope(q, k, *fa.rope_table(8, 64), q_out=torch.empty_like(q), k_out=torch.empty_like(k))
+    with pytest.raises(fa.FaError):
+        fa.decode_sinks(q[:, :, 0].contiguous(), k, k, torch.zeros(0, dtype=torch.int32, device="cuda"), 4, 1,
+                        out=torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16))
