@@ -21,7 +21,10 @@
 // holds whole pairs (columns 8 l and rot/2 + 8 l on, or 16 l on when
 // interleaved): no exchange between lanes but the row's sum.  A warp keeps its
 // tokens' eight cos / sin values a lane in registers and walks over heads of one
-// operand, the next row on its way.
+// operand, the next row on its way.  Measured, 16384 tokens x 18 heads of 128, inputs
+// not in L2: forward 28.8 us (23.4 at the measured copy rate), issue slots 58% used;
+// gradient 53.4 us (34.9), where registers leave 16 warps an SM, issue slots are 43%
+// used and the wait for loads is the largest part of a warp's time.
 #pragma once
 
 #include "fa_fwd_sm100.cuh"

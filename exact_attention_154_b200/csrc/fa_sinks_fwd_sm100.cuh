@@ -5,7 +5,8 @@
 //   keys j <= i with i - j <= window or j < sinks; LSE_i = ln sum_j exp(s_ij)
 //
 // by the online recurrence of fa_fwd_sm100.cuh (running reference, lazily moved;
-// row sum and O in fp32; 16-bit weights before P V).
+// row sum and O in fp32).  The weights are rounded to 16 bits before P V, since one
+// matrix instruction takes P and V in one type; the row sum adds them unrounded.
 //
 // What bounds it under a window: latency.  A 128-row query tile meets only
 // window / 64 + 3 blocks of 64 keys, so the chain of a block (scores,
@@ -30,11 +31,14 @@
 // blocks are those holding sinks, then the window's.  Every wait is bounded.
 //
 // Measured (bf16, d = 128, 16 query heads on 2; inputs not in L2): window 256, 4 x
-// 4096 rows, 76 us; window 4096, 16384 rows, 519 us (928 TFLOP/s of visible pairs);
-// 2 x 12 heads of 333 rows at d = 64, 8.2 us.  The plain forward's shape given the
+// 4096 rows, 77 us; window 4096, 16384 rows, 525 us (917 TFLOP/s of visible pairs);
+// 2 x 12 heads of 333 rows at d = 64, 8.3 us.  The plain forward's shape given the
 // same masks (128-key blocks, two tiles and four softmax warpgroups a CTA, one CTA
-// an SM, P in shared memory) took 111, 519 and 12.2 us.  Under the wide window the
-// two CTAs of an SM take 1860 cycles a block each; the tensor pipe is busy 72% of
+// an SM, P in shared memory) took 111, 519 and 12.2 us.  By clocks read in a copy, window
+// 256 takes 15,900 cycles a tile of 6.7 blocks: a block 1140 of work on its scores, 400
+// of bounds and loop before them, 200 of waiting; the tile's first scores 1040, its last
+// P V 1530, its output 1800.  Under the wide window the
+// two CTAs of an SM take 1880 cycles a block each; the tensor pipe is busy 72% of
 // them (54% of its rate: a product with 64 keys on its wide side reads its 128
 // query rows for half as many columns), the exponential unit 53%.  A part of the
 // exponentials as a polynomial on the FMA pipe, and P handed over in halves, were no
